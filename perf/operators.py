@@ -229,7 +229,7 @@ def _plan(s):
         p["args"] = kv.window_args(s["q"], s["out"], s["pos"], s["length"], s["longest"], window=c["window"],
                                    sinks=c["sinks"], cu_seqlens=s["cu"] if s["most"] > 1 else None,
                                    max_tokens_per_req=s["most"])
-        p["workspace"] = kv.window_workspace(p["ctx"], p["args"])
+        p["workspace"] = kv.window_workspace(p["ctx"])
     return p
 
 
