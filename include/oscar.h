@@ -426,6 +426,194 @@ oscar_status oscar_calib_clip_threshold(oscar_ctx* ctx, const float* x, int64_t 
                                         uint32_t flags, double percentile, double* tau, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged caches whose tokens are all of one kind, with positions rotated on
+ * the way in: the BF16 pages of oscar_bf16_cache_view and a cache held in 4
+ * bits.  No passage of the pages covers them: these are services of this
+ * library for the layers and models that keep such a cache beside (or in
+ * place of) the mixed INT2 one -- layers too sensitive for 2 bits, and layers
+ * that attend a sliding window.  They need no loaded rotation.
+ *
+ * Conventions of the calls below, beside those at the top: a request's
+ * positions [64 i, 64 i + 64) live in the page that entry i of its table row
+ * names, entry 0 included.  Entries of pages that a call neither reads nor
+ * writes are not looked at (the pages that left a window may be given back).
+ * cu_seqlens and max_tokens_per_req are as in oscar_append_args; requests
+ * whose cu_seqlens are inconsistent with n_tokens, or that own more than
+ * max_tokens_per_req tokens, are skipped (OSCAR_DEVERR_TOKENS), and rows of no
+ * request are left as they were.  A call is one launch, so it can be captured
+ * into a graph.
+ */
+
+/*
+ * The cache held in 4 bits.  A block (one page of one KV head) is four tiles
+ * of 16 tokens, 2176 bytes each:
+ *   [   0, 1024)  K codes      [1024, 2048)  V codes
+ *   [2048, 2112)  K scales fp16 [16 tokens][2 groups]
+ *   [2112, 2176)  V scales fp16 [16 tokens][2 groups]
+ * What is stored is x' = x H / sqrt(128), H the 128-point Hadamard matrix in
+ * Sylvester order ([IT] "I tre fattori della rotazione": the Hadamard factor
+ * spreads a channel that stands out over all of them; 4 bits need no
+ * calibrated basis).  Per token and group of 64 rotated channels
+ * a = max|x'|, s = fp16(min(a, 65504 * 7.5) / 7.5), code
+ * c = floor(x' / s + 8) clamped to 0..15 (8 when s is 0); a code stands for
+ * the level (c - 7.5) s.  A row that holds a NaN or an infinity gets
+ * unspecified codes.  With u = token % 16, rotated channel j (bits j0..j6):
+ *   K: byte 64 u + 16 (j / 8 % 4) + 4 (j / 32) + n / 2, nibble n % 2,
+ *      n = 4 j0 + 2 j2 + j1
+ *   V: byte 512 j6 + 16 (4 (j % 4 + 4 j3) + u % 8 / 2) + 4 (j2 + 2 j5)
+ *      + 2 (u % 2) + u / 8, nibble j4
+ */
+#define OSCAR_INT4_TILE_BYTES 2176
+#define OSCAR_INT4_BLOCK_BYTES 8704
+
+/*
+ *   pages       [num_pages][num_kv_heads][OSCAR_INT4_BLOCK_BYTES] bytes, device,
+ *               16-byte aligned.
+ *   page_table  device int32 [batch][max_pages_per_req].
+ */
+typedef struct {
+  void* pages;
+  int64_t num_pages;
+  const int32_t* page_table;
+  int32_t max_pages_per_req;
+  int32_t batch;
+} oscar_int4_cache_view;
+
+/*
+ * New tokens of an append with position rotation.
+ *   q, k, v   device bf16 [n_tokens][heads][128], 16-byte aligned; the elements
+ *             from one token to the next are q_stride, k_stride, v_stride
+ *             (multiples of 8, at least heads * 128; 0: heads * 128), so the
+ *             three may be parts of one projection's output.  q NULL: no
+ *             queries.
+ *   q_out     device bf16 [n_tokens][num_q_heads][128], the rotated queries,
+ *             q_out_stride elements apart (0: num_q_heads * 128); may be q
+ *             itself with q's stride.
+ *   rope      device fp32 [rope_positions][rotary_dim], 16-byte aligned: row p
+ *             holds cos(p f_i), then sin(p f_i), for i < rotary_dim / 2
+ *             (oscar_rope_table fills it).  NULL when rotary_dim is 0.
+ *   rotary_dim  channels that are rotated, from channel 0: 0, 64 or 128 (other
+ *             values: OSCAR_ERR_UNSUPPORTED); the rest pass through.
+ *   interleaved  0: channel i turns with channel i + rotary_dim / 2;
+ *             1: channel 2 i with channel 2 i + 1.
+ *   pos       device int32 [batch]: position of each request's first new token.
+ * A pair (x, y) becomes (x cos - y sin, y cos + x sin), computed in fp32 and
+ * rounded once to bf16; v is not rotated.
+ */
+typedef struct {
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  int64_t q_stride;
+  int64_t q_out_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const float* rope;
+  int32_t rope_positions;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  const int32_t* pos;
+  const int32_t* cu_seqlens;
+  int32_t n_tokens;
+  int32_t max_tokens_per_req;
+} oscar_rope_append_args;
+
+/* Fill a rope table: row p, column i: cos(p theta^(-2i / rotary_dim)), column
+ * rotary_dim / 2 + i its sine; the angle in fp64 (a far position's angle needs
+ * more than 24 bits), the entries rounded to fp32.  table: device fp32
+ * [n_positions][rotary_dim]; theta positive and finite; rotary_dim 64 or 128. */
+oscar_status oscar_rope_table(oscar_ctx* ctx, float* table, int32_t n_positions, int32_t rotary_dim, double theta,
+                              void* stream);
+
+/*
+ * Rotate the new tokens' q and k by their positions and write k and v into the
+ * pages.  The view's pools are written here (its pointers are const for the
+ * calls that only read).  A token whose position is negative, beyond the rope
+ * table or beyond the page table is skipped with OSCAR_DEVERR_LENGTH (its q_out
+ * row too), one whose page is not in the pool with OSCAR_DEVERR_PAGE (its q_out
+ * row is written).  The caller never lets two requests append to one page.
+ */
+oscar_status oscar_rope_append_bf16(oscar_ctx* ctx, const oscar_bf16_cache_view* view,
+                                    const oscar_rope_append_args* args, void* stream);
+
+/* The same into the 4-bit cache: the rotated, bf16-rounded k (what the BF16
+ * pages would hold) and v go through the Hadamard factor and the quantiser.
+ * Tokens may be appended one at a time or many: a token's codes share no byte
+ * with another's. */
+oscar_status oscar_rope_append_int4(oscar_ctx* ctx, const oscar_int4_cache_view* view,
+                                    const oscar_rope_append_args* args, void* stream);
+
+/*
+ * Read rows of the 4-bit cache back into BF16 pages (for a chunk's attention
+ * over a prefix held in 4 bits): positions [pos[b], pos[b] + count[b]) of every
+ * request, as the values they stand for in the original basis,
+ * bf16((c - 7.5) s H / sqrt(128)), into the same positions of the BF16 view.
+ * pos, count: device int32 [batch]; max_count: host upper bound of count
+ * (a larger count: OSCAR_DEVERR_TOKENS, the request is skipped).  The views
+ * have the same batch; a position outside either page table sets
+ * OSCAR_DEVERR_LENGTH, a page outside either pool OSCAR_DEVERR_PAGE.
+ */
+oscar_status oscar_int4_to_bf16(oscar_ctx* ctx, const oscar_int4_cache_view* from, const oscar_bf16_cache_view* to,
+                                const int32_t* pos, const int32_t* count, int32_t max_count, void* stream);
+
+/*
+ * Attention with a sliding window and a few first tokens that stay visible.
+ * The query at position p sees the positions j <= p, j < ctx_len[b], with
+ * j < sinks or j > p - window.
+ *   q        device bf16 [n_tokens][num_q_heads][128] (rotated by position, as
+ *            the append leaves it), 16-byte aligned, q_stride elements from one
+ *            token to the next (a multiple of 8; 0: num_q_heads * 128).
+ *   out      device bf16 [n_tokens][num_q_heads][128], 16-byte aligned.  The
+ *            sums run in fp32; only the result is rounded, for the projection
+ *            that reads it.  A query that sees nothing gets zeros.
+ *   pos      device int32 [batch]: position of each request's first query.  A
+ *            negative position sets OSCAR_DEVERR_LENGTH (zeros).
+ *   ctx_len  device int32 [batch]: positions that the cache holds (below
+ *            them every visible position's page must be in the table).
+ *   max_ctx_len  host upper bound of ctx_len (sizes the launch; a larger
+ *            ctx_len is still attended, only less evenly split).
+ *   window   visible positions up to the query's own; negative: all of them;
+ *            0: the sinks alone.
+ *   sinks    first positions that stay visible (>= 0).
+ *   sm_scale softmax scale; <= 0 selects 1/sqrt(128).
+ * Cache rows that no query of the call sees may hold anything, NaN included.
+ */
+typedef struct {
+  const void* q;
+  void* out;
+  const int32_t* pos;
+  const int32_t* cu_seqlens;
+  const int32_t* ctx_len;
+  int64_t q_stride;
+  int32_t n_tokens;
+  int32_t max_tokens_per_req;
+  int32_t max_ctx_len;
+  int32_t window;
+  int32_t sinks;
+  float sm_scale;
+} oscar_window_args;
+
+/* Workspace bytes of the two calls below: one size for every call on the context. */
+size_t oscar_window_workspace_bytes(const oscar_ctx* ctx);
+
+/*
+ * Over the BF16 pages (16-byte aligned pools), and over the 4-bit cache (the
+ * queries are turned by H, the result turned back).  workspace: device,
+ * 256-byte aligned, at least oscar_window_workspace_bytes(ctx) bytes; zeros
+ * before its first use, left reusable by every call; calls that share one must
+ * not overlap on the GPU (two captured graphs that share one, too).  A visible
+ * position outside the page table sets OSCAR_DEVERR_LENGTH and a page outside
+ * the pool OSCAR_DEVERR_PAGE; such positions are left out.
+ */
+oscar_status oscar_window_attention_bf16(oscar_ctx* ctx, const oscar_bf16_cache_view* view,
+                                         const oscar_window_args* args, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+oscar_status oscar_window_attention_int4(oscar_ctx* ctx, const oscar_int4_cache_view* view,
+                                         const oscar_window_args* args, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
 /* Synchronise the stream, return and clear the device error word in *bits
  * (may be NULL).  Returns OSCAR_ERR_DEVICE_CHECK when any bit was set. */
 oscar_status oscar_check_device_error(oscar_ctx* ctx, void* stream, uint32_t* bits);

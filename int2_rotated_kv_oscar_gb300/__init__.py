@@ -10,4 +10,6 @@ rotations and clip thresholds.
 from . import abi  # noqa: F401
 from .abi import (OscarError, oscar_check_device_error, oscar_create, oscar_decode_attention,  # noqa: F401
                   oscar_decode_attention_bf16, oscar_decode_workspace_bytes, oscar_destroy,
-                  oscar_device_sm_count, oscar_kv_append, oscar_load_rotation, oscar_status_string)
+                  oscar_device_sm_count, oscar_int4_to_bf16, oscar_kv_append, oscar_load_rotation,
+                  oscar_rope_append_bf16, oscar_rope_append_int4, oscar_rope_table, oscar_status_string,
+                  oscar_window_attention_bf16, oscar_window_attention_int4, oscar_window_workspace_bytes)

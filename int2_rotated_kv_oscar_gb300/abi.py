@@ -18,6 +18,8 @@ GROUP = 64
 MAX_GQA = 8
 BLOCK_BYTES = 4608
 NOALLOC_SCRATCH_BYTES = 16 << 20
+INT4_TILE_BYTES = 2176
+INT4_BLOCK_BYTES = 8704
 
 OSCAR_OK = 0
 STATUS_NAMES = {0: "OSCAR_OK", 1: "OSCAR_ERR_INVALID_ARG", 2: "OSCAR_ERR_UNSUPPORTED", 3: "OSCAR_ERR_NOT_LOADED",
@@ -75,6 +77,27 @@ class oscar_bf16_cache_view(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("max_pages_per_req", ctypes.c_int32), ("batch", ctypes.c_int32)]
 
 
+class oscar_int4_cache_view(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("max_pages_per_req", ctypes.c_int32), ("batch", ctypes.c_int32)]
+
+
+class oscar_rope_append_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("rope", ctypes.c_void_p), ("rope_positions", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("pos", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("n_tokens", ctypes.c_int32),
+                ("max_tokens_per_req", ctypes.c_int32)]
+
+
+class oscar_window_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int32), ("max_tokens_per_req", ctypes.c_int32), ("max_ctx_len", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("sm_scale", ctypes.c_float)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "oscar_create": (ctypes.c_int, [ctypes.POINTER(oscar_config), ctypes.POINTER(ctypes.c_void_p)]),
@@ -112,6 +135,22 @@ SIGNATURES = {
     "oscar_calib_clip_threshold": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                                   ctypes.c_uint32, ctypes.c_double, ctypes.POINTER(ctypes.c_double),
                                                   ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "oscar_rope_table": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.c_double, ctypes.c_void_p]),
+    "oscar_rope_append_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(oscar_bf16_cache_view),
+                                              ctypes.POINTER(oscar_rope_append_args), ctypes.c_void_p]),
+    "oscar_rope_append_int4": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(oscar_int4_cache_view),
+                                              ctypes.POINTER(oscar_rope_append_args), ctypes.c_void_p]),
+    "oscar_int4_to_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(oscar_int4_cache_view),
+                                          ctypes.POINTER(oscar_bf16_cache_view), ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_int32, ctypes.c_void_p]),
+    "oscar_window_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p]),
+    "oscar_window_attention_bf16": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(oscar_bf16_cache_view),
+                                                   ctypes.POINTER(oscar_window_args), ctypes.c_void_p,
+                                                   ctypes.c_size_t, ctypes.c_void_p]),
+    "oscar_window_attention_int4": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(oscar_int4_cache_view),
+                                                   ctypes.POINTER(oscar_window_args), ctypes.c_void_p,
+                                                   ctypes.c_size_t, ctypes.c_void_p]),
     "oscar_check_device_error": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
     "oscar_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p]),
     "oscar_device_sm_count": (ctypes.c_int32, [ctypes.c_void_p]),
@@ -267,6 +306,46 @@ def oscar_calib_clip_threshold(ctx, x, n_rows, U, flags, percentile, workspace, 
                                              ctypes.byref(tau), _ptr(workspace), workspace_bytes, _stream(stream)),
            "oscar_calib_clip_threshold")
     return float(tau.value)
+
+
+def oscar_rope_table(ctx, table, theta, stream=None):
+    """Fill a device float32 table [n_positions, rotary_dim] with cos and sin of the position angles."""
+    _check(load().oscar_rope_table(ctx, _ptr(table), table.shape[0], table.shape[1], float(theta), _stream(stream)),
+           "oscar_rope_table")
+
+
+def oscar_rope_append_bf16(ctx, view, args, stream=None):
+    """Rotate the new tokens' q and k by position and write k, v into BF16 pages."""
+    _check(load().oscar_rope_append_bf16(ctx, ctypes.byref(view), ctypes.byref(args), _stream(stream)),
+           "oscar_rope_append_bf16")
+
+
+def oscar_rope_append_int4(ctx, view, args, stream=None):
+    """Rotate the new tokens' q and k by position and write k, v into the 4-bit cache."""
+    _check(load().oscar_rope_append_int4(ctx, ctypes.byref(view), ctypes.byref(args), _stream(stream)),
+           "oscar_rope_append_int4")
+
+
+def oscar_int4_to_bf16(ctx, from_view, to_view, pos, count, max_count, stream=None):
+    """Read positions [pos, pos + count) of every request (device int32) back from the 4-bit cache into BF16 pages."""
+    _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), _ptr(pos), _ptr(count),
+                                     max_count, _stream(stream)), "oscar_int4_to_bf16")
+
+
+def oscar_window_workspace_bytes(ctx):
+    return int(load().oscar_window_workspace_bytes(ctx))
+
+
+def oscar_window_attention_bf16(ctx, view, args, workspace, workspace_bytes, stream=None):
+    """Attention with a sliding window and visible first tokens over BF16 pages."""
+    _check(load().oscar_window_attention_bf16(ctx, ctypes.byref(view), ctypes.byref(args), _ptr(workspace),
+                                              workspace_bytes, _stream(stream)), "oscar_window_attention_bf16")
+
+
+def oscar_window_attention_int4(ctx, view, args, workspace, workspace_bytes, stream=None):
+    """The same over the 4-bit cache."""
+    _check(load().oscar_window_attention_int4(ctx, ctypes.byref(view), ctypes.byref(args), _ptr(workspace),
+                                              workspace_bytes, _stream(stream)), "oscar_window_attention_int4")
 
 
 def oscar_selftest_bounded_wait(ctx, polls, stream=None):

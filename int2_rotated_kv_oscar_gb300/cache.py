@@ -128,6 +128,102 @@ def decode_args(q, out, ctx_len, max_ctx_len, sm_scale=0.0):
     return a
 
 
+class Int4PagedCache:
+    """The 4-bit paged cache of one layer: pages uint8 [num_pages, Hkv, 8704], page_table int32 [batch, max_pages]."""
+
+    def __init__(self, num_kv_heads, num_pages, batch, max_pages_per_req, device="cuda"):
+        self.pages = torch.zeros((num_pages, num_kv_heads, abi.INT4_BLOCK_BYTES), dtype=torch.uint8, device=device)
+        self.page_table = torch.zeros((batch, max_pages_per_req), dtype=torch.int32, device=device)
+
+    def view(self):
+        return int4_view(self.pages, self.page_table)
+
+
+def int4_view(pages, page_table):
+    """oscar_int4_cache_view of contiguous pages uint8 [num_pages, Hkv, 8704] and page_table int32 [batch, max_pages].
+    The struct keeps the tensors alive for as long as it lives (it holds their addresses)."""
+    _contiguous(pages, page_table)
+    v = abi.oscar_int4_cache_view(pages=pages.data_ptr(), num_pages=pages.shape[0], page_table=page_table.data_ptr(),
+                                  max_pages_per_req=page_table.shape[1], batch=page_table.shape[0])
+    v._tensors = (pages, page_table)
+    return v
+
+
+def bf16_view(k_pages, v_pages, page_table):
+    """oscar_bf16_cache_view of contiguous pools bf16 [num_pages, Hkv, 64, 128] and page_table int32 [batch, max_pages]."""
+    _contiguous(k_pages, v_pages, page_table)
+    v = abi.oscar_bf16_cache_view(k_pages=k_pages.data_ptr(), v_pages=v_pages.data_ptr(), num_pages=k_pages.shape[0],
+                                  page_table=page_table.data_ptr(), max_pages_per_req=page_table.shape[1],
+                                  batch=page_table.shape[0])
+    v._tensors = (k_pages, v_pages, page_table)
+    return v
+
+
+def _contiguous(*tensors):
+    if not all(t.is_contiguous() for t in tensors):
+        raise ValueError("pools and page tables must be contiguous")
+
+
+def _token_stride(x, name):
+    """Elements from one token to the next of x [n_tokens, heads, 128], whose rows of a token must be packed."""
+    if x.dim() != 3 or x.shape[2] != abi.HEAD_DIM or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != abi.HEAD_DIM):
+        raise ValueError("%s must be [n_tokens, heads, 128] with packed heads" % name)
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * abi.HEAD_DIM
+
+
+def rope_table(ctx, n_positions, rotary_dim=128, theta=1e6, device="cuda"):
+    """The position table float32 [n_positions, rotary_dim] that rope_append_args takes."""
+    t = torch.empty((n_positions, rotary_dim), dtype=torch.float32, device=device)
+    abi.oscar_rope_table(ctx, t, theta, torch.cuda.current_stream(t.device))
+    return t
+
+
+def rope_append_args(k, v, pos, q=None, q_out=None, rope=None, interleaved=False, cu_seqlens=None,
+                     max_tokens_per_req=None):
+    """oscar_rope_append_args for bf16 k, v [n_tokens, Hkv, 128], optional q and q_out [n_tokens, Hq, 128] (all may be
+    slices of a wider row) and a float32 rope table [n_positions, rotary_dim] (None: no rotation).
+    The struct keeps the tensors alive."""
+    n = int(k.shape[0])
+    if rope is not None:
+        _contiguous(rope)
+    a = abi.oscar_rope_append_args(
+        q=None if q is None else q.data_ptr(), q_out=None if q_out is None else q_out.data_ptr(), k=k.data_ptr(),
+        v=v.data_ptr(), q_stride=0 if q is None else _token_stride(q, "q"),
+        q_out_stride=0 if q_out is None else _token_stride(q_out, "q_out"), k_stride=_token_stride(k, "k"),
+        v_stride=_token_stride(v, "v"), rope=None if rope is None else rope.data_ptr(),
+        rope_positions=0 if rope is None else rope.shape[0], rotary_dim=0 if rope is None else rope.shape[1],
+        interleaved=1 if interleaved else 0, pos=pos.data_ptr(),
+        cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr(), n_tokens=n,
+        max_tokens_per_req=n if max_tokens_per_req is None else int(max_tokens_per_req))
+    a._tensors = (q, q_out, k, v, rope, pos, cu_seqlens)
+    return a
+
+
+def window_args(q, out, pos, ctx_len, max_ctx_len, window=-1, sinks=0, cu_seqlens=None, max_tokens_per_req=None,
+                sm_scale=0.0):
+    """oscar_window_args for bf16 q [n_tokens, Hq, 128] (may be a slice of a wider row) and contiguous bf16 out.
+    The struct keeps the tensors alive."""
+    _contiguous(out)
+    n = int(q.shape[0])
+    a = abi.oscar_window_args(
+        q=q.data_ptr(), out=out.data_ptr(), pos=pos.data_ptr(),
+        cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr(), ctx_len=ctx_len.data_ptr(),
+        q_stride=_token_stride(q, "q"), n_tokens=n,
+        max_tokens_per_req=(1 if cu_seqlens is None else n) if max_tokens_per_req is None else int(max_tokens_per_req),
+        max_ctx_len=int(max_ctx_len), window=int(window), sinks=int(sinks), sm_scale=float(sm_scale))
+    a._tensors = (q, out, pos, cu_seqlens, ctx_len)
+    return a
+
+
+def window_workspace(ctx, device="cuda"):
+    """A caller-owned workspace for the context's oscar_window_attention_* calls (256-byte aligned, zero-filled).
+    Returns (tensor, pointer, bytes)."""
+    n = abi.oscar_window_workspace_bytes(ctx)
+    t = torch.zeros(n + 256, dtype=torch.uint8, device=device)
+    off = (-t.data_ptr()) % 256
+    return t, t.data_ptr() + off, n
+
+
 def extend_workspace(ctx, batch, chunk, max_ctx_len, device="cuda"):
     """A caller-owned workspace for oscar_extend_chunk (uint8 tensor, 256-byte
     aligned, zero-filled).  Returns (tensor, pointer, bytes)."""

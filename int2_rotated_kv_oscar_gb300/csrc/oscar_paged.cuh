@@ -1,0 +1,81 @@
+// Device helpers of the one-kind paged caches: spans of new tokens, page
+// lookups, the pieces of the 4-bit layout (include/oscar.h) and the 128-point
+// Hadamard transform on the tensor cores.
+#pragma once
+
+#include "oscar_device.cuh"
+#include "oscar_internal.h"
+#include "oscar_paged.h"
+
+namespace oscar {
+namespace {
+
+// Request b's tokens: the first one's position, how many, and their first row.
+__device__ __forceinline__ bool token_span(const TokenRefs& t, int b, int& p0, int& n, int& row0, unsigned* err,
+                                           bool report) {
+  p0 = t.pos[b];
+  row0 = b;
+  n = 1;
+  if (t.cu != nullptr) {
+    const int lo = t.cu[b], hi = t.cu[b + 1];
+    if (lo < 0 || hi < lo || hi > t.n_tokens || hi - lo > t.max_tokens) {
+      if (report) set_error(err, kErrTokens);
+      return false;
+    }
+    row0 = lo;
+    n = hi - lo;
+  }
+  return true;
+}
+
+// Physical page of logical page lp (known to be inside the table) of request b, -1 with an error bit if bad.
+__device__ __forceinline__ int page_of(const PageRefs& p, int b, int lp, unsigned* err, bool report) {
+  const int phys = p.table[(size_t)b * p.max_pages + lp];
+  if (phys >= 0 && phys < p.num_pages) return phys;
+  if (report) set_error(err, kErrPage);
+  return -1;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t& word_of(uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Turn eight pairs: a = (x0..x7), b = (y0..y7) as bf16, c and s their cosines and sines.
+__device__ __forceinline__ void turn8(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t ua = word_of(a, i), ub = word_of(b, i);
+    const float x0 = bf16_lo(ua), x1 = bf16_hi(ua), y0 = bf16_lo(ub), y1 = bf16_hi(ub);
+    word_of(a, i) = pack_bf16x2(fmaf(x0, c[2 * i], -y0 * s[2 * i]), fmaf(x1, c[2 * i + 1], -y1 * s[2 * i + 1]));
+    word_of(b, i) = pack_bf16x2(fmaf(y0, c[2 * i], x0 * s[2 * i]), fmaf(y1, c[2 * i + 1], x1 * s[2 * i + 1]));
+  }
+}
+
+// Turn four adjacent pairs held in one 16-byte piece.
+__device__ __forceinline__ void turn4(uint4& a, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = word_of(a, i);
+    const float x = bf16_lo(u), y = bf16_hi(u);
+    word_of(a, i) = pack_bf16x2(fmaf(x, c[i], -y * s[i]), fmaf(y, c[i], x * s[i]));
+  }
+}
+
+__device__ __forceinline__ void load8(float (&v)[8], const float* p) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+__device__ __forceinline__ void load4(float* v, const float* p) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+}
+
+__device__ __forceinline__ int odd_bits(int x) { return __popc((unsigned)x) & 1; }
+
+}  // namespace
+}  // namespace oscar

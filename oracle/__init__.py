@@ -33,6 +33,7 @@ Modules:
                   (token, channel) -> (byte, bit) map).
 * ``cache``       sink / recent / history segments; the append/eviction model.
 * ``attention``   softmax attention in fp64; decode over a mixed cache.
+* ``paged``       position rotation, the 4-bit cache and windowed attention.
 * ``calibration`` offline C_Q, C_S, eigenbases and clip thresholds.
 
 Every public function is pinned by a ``-m "not gpu"`` test in
@@ -42,4 +43,4 @@ Functions without such a pin say "parity unpinned" in their docstring; at
 present there are none.
 """
 
-from . import rotation, quant, layout, cache, attention, calibration  # noqa: F401
+from . import rotation, quant, layout, cache, attention, calibration, paged  # noqa: F401
