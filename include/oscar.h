@@ -568,8 +568,8 @@ oscar_status oscar_int4_to_bf16(oscar_ctx* ctx, const oscar_int4_cache_view* fro
  *   out      device bf16 [n_tokens][num_q_heads][128], 16-byte aligned.  The
  *            sums run in fp32; only the result is rounded, for the projection
  *            that reads it.  A query that sees nothing gets zeros.
- *   pos      device int32 [batch]: position of each request's first query.  A
- *            negative position sets OSCAR_DEVERR_LENGTH (zeros).
+ *   pos      device int32 [batch]: position of each request's first query (a
+ *            negative one sets OSCAR_DEVERR_LENGTH: zeros for the request).
  *   ctx_len  device int32 [batch]: positions that the cache holds (below
  *            them every visible position's page must be in the table).
  *   max_ctx_len  host upper bound of ctx_len (sizes the launch; a larger
@@ -579,6 +579,8 @@ oscar_status oscar_int4_to_bf16(oscar_ctx* ctx, const oscar_int4_cache_view* fro
  *   sinks    first positions that stay visible (>= 0).
  *   sm_scale softmax scale; <= 0 selects 1/sqrt(128).
  * Cache rows that no query of the call sees may hold anything, NaN included.
+ * A V row that is not finite may reach, beside the queries that see it, others
+ * of its request (their tile of 128 rows).
  */
 typedef struct {
   const void* q;

@@ -60,7 +60,7 @@ cudaError_t launch_int4_to_bf16(const Read4Launch& a, cudaStream_t stream);
 // visible keys are cut into `items` work items, one block each).
 struct WindowPlan {
   int32_t items = 1;
-  size_t off_records = 0, total = 0;  // workspace: counters [rows][Hkv], records [rows][Hkv][items]; one size for all calls
+  size_t off_records = 0, total = 0;  // workspace: counters, then the items' records; one size for all calls
 };
 
 struct WindowLaunch {
@@ -82,5 +82,10 @@ struct WindowLaunch {
 };
 WindowPlan plan_window(bool int4, int64_t rows, int Hq, int Hkv, int64_t max_keys, int num_sms);
 cudaError_t launch_window_split(const WindowLaunch& a, cudaStream_t stream);
+
+// Chunks and prompts over BF16 pages, on the tensor cores (records [blocks][256 rows][130] of its items).
+constexpr int kTcSplitBlocks = 2;  // blocks per SM that one call may split its keys over
+WindowPlan plan_window_tc(int64_t batch, int64_t max_tokens, int Hq, int Hkv, int64_t max_keys, int num_sms);
+cudaError_t launch_window_tc(const WindowLaunch& a, cudaStream_t stream);
 
 }  // namespace oscar

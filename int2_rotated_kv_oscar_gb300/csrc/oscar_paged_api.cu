@@ -98,6 +98,9 @@ int64_t max_visible(int32_t max_ctx, int32_t window, int32_t sinks) {
   return window < 0 ? max_ctx : std::min<int64_t>(max_ctx, (int64_t)window + sinks);
 }
 
+// Chunks and prompts over BF16 pages take the tensor-core kernel.
+bool on_tensor_cores(const WindowLaunch& a, bool int4) { return !int4 && a.tok.max_tokens > 1; }
+
 oscar_status window_launch(const oscar_ctx* ctx, const oscar_window_args* args, int32_t batch, bool int4, void* ws,
                            size_t ws_bytes, WindowLaunch* a) {
   const oscar_status st = tokens_of(args->pos, args->cu_seqlens, args->n_tokens, args->max_tokens_per_req, batch, &a->tok);
@@ -116,9 +119,11 @@ oscar_status window_launch(const oscar_ctx* ctx, const oscar_window_args* args, 
   a->Hkv = ctx->cfg.num_kv_heads;
   a->num_sms = ctx->num_sms;
   a->err = ctx->d_err;
-  a->plan = plan_window(int4, args->n_tokens, a->Hq, a->Hkv, max_visible(args->max_ctx_len, args->window, args->sinks),
-                        ctx->num_sms);
-  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < a->plan.total) return OSCAR_ERR_WORKSPACE;
+  const int64_t keys = max_visible(args->max_ctx_len, args->window, args->sinks);
+  a->plan = on_tensor_cores(*a, int4)
+                ? plan_window_tc(batch, a->tok.max_tokens, a->Hq, a->Hkv, keys, ctx->num_sms)
+                : plan_window(int4, args->n_tokens, a->Hq, a->Hkv, keys, ctx->num_sms);
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < oscar_window_workspace_bytes(ctx)) return OSCAR_ERR_WORKSPACE;
   a->workspace = static_cast<uint8_t*>(ws);
   if ((int64_t)args->n_tokens * a->plan.items > INT32_MAX) return OSCAR_ERR_UNSUPPORTED;
   return OSCAR_OK;
@@ -198,7 +203,9 @@ oscar_status oscar_int4_to_bf16(oscar_ctx* ctx, const oscar_int4_cache_view* fro
 }
 
 size_t oscar_window_workspace_bytes(const oscar_ctx* ctx) {
-  return ctx == nullptr ? 0 : plan_window(true, 1, ctx->cfg.num_q_heads, ctx->cfg.num_kv_heads, 0, ctx->num_sms).total;
+  if (ctx == nullptr) return 0;
+  const int Hq = ctx->cfg.num_q_heads, Hkv = ctx->cfg.num_kv_heads;
+  return std::max(plan_window(false, 1, Hq, Hkv, 0, ctx->num_sms).total, plan_window_tc(1, 1, Hq, Hkv, 0, ctx->num_sms).total);
 }
 
 oscar_status oscar_window_attention_bf16(oscar_ctx* ctx, const oscar_bf16_cache_view* view,
@@ -215,7 +222,8 @@ oscar_status oscar_window_attention_bf16(oscar_ctx* ctx, const oscar_bf16_cache_
   a.k_pages = static_cast<const uint16_t*>(view->k_pages);
   a.v_pages = static_cast<const uint16_t*>(view->v_pages);
   DeviceGuard guard(ctx->cfg.device);
-  return status_of(launch_window_split(a, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return status_of(on_tensor_cores(a, false) ? launch_window_tc(a, s) : launch_window_split(a, s));
 }
 
 oscar_status oscar_window_attention_int4(oscar_ctx* ctx, const oscar_int4_cache_view* view,

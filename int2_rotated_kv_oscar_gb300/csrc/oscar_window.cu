@@ -112,7 +112,7 @@ __device__ __forceinline__ bool seen_by(const WindowLaunch& a, int i, int& b, Se
   if (!token_span(a.tok, b, p0, n, row0, a.err, report) || i < row0 || i >= row0 + n) return false;
   const long long p = (long long)p0 + (i - row0);
   long long len = min(p + 1, (long long)max(a.ctx_len[b], 0));
-  if (p < 0) {
+  if (p0 < 0) {
     if (report) set_error(a.err, kErrLength);
     len = 0;
   }
