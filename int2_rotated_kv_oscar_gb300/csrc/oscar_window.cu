@@ -42,6 +42,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool r
   const unsigned n = real ? 16u : 0u;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
+  const unsigned n = real ? 8u : 0u;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -84,10 +88,6 @@ struct Seen {
   __device__ __forceinline__ int tiles() const { return s_end + max(0, w_end - w_begin); }
   __device__ __forceinline__ int tile(int t) const { return t < s_end ? t : w_begin + (t - s_end); }
   __device__ __forceinline__ bool sees(int j) const { return j < len && (j < sinks || j >= low); }
-  // whether a query sees all of tile T
-  __device__ __forceinline__ bool whole(int T) const {
-    return 16 * T + 16 <= len && (16 * T + 16 <= sinks || 16 * T >= low);
-  }
 };
 
 // The request of token row i.
@@ -149,7 +149,7 @@ __device__ __forceinline__ void copy_unit(const WindowLaunch& a, const Seen& s, 
         a.pages4 + ((size_t)max(phys, 0) * a.Hkv + h) * kBlock4Bytes + (size_t)(T & 3) * kTile4Bytes + 16 * lane;
 #pragma unroll
     for (int i = 0; i < 8; ++i) cp_async16(stage + 16 * lane + 512 * i, src + 512 * i, phys >= 0);
-    if (lane < 16) cp_async16(stage + 16 * lane + 4096, src + 4096, phys >= 0);
+    cp_async8(stage + 8 * lane + 4096, src - 8 * lane + 4096, phys >= 0);
   } else {
     const size_t off = ((size_t)max(phys, 0) * a.Hkv + h) * (kPage * kD) + (size_t)(T & 3) * 16 * kD;
     const uint4* k = reinterpret_cast<const uint4*>(a.k_pages + off);
@@ -174,15 +174,25 @@ struct State {
   float o[8][4];
 };
 
-// 4-bit words to bf16 pairs.  K: 128 + c from the bits alone.  V: 16 + c: a smaller offset, because
-// P V cancels it against the sum of the weights and the MMA's fp32 sums truncate relative to it
-// (the logits' offset is cancelled inside one tile's product).
-__device__ __forceinline__ uint32_t k_pair(uint32_t w, int i) {
-  return ((i == 0 ? w : w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+// 4-bit words to bf16 pairs, from the bits alone.  K: 128 + c.  V: 16 + c: a smaller offset, because P V
+// cancels it against the sum of the weights and the MMA's fp32 sums truncate relative to it (the logits'
+// offset is cancelled inside one tile's product).  The exponent bits come in a register, so that masking
+// and setting them is one LOP3 (as two constants they were two: 64 of 370 instructions a tile).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
 }
-__device__ __forceinline__ uint32_t v_pair(uint32_t w, int i) {
-  const uint32_t x = i == 0 ? w << 3 : w >> (4 * i - 3);
-  return (x & 0x00780078u) | 0x41804180u;
+__device__ __forceinline__ uint32_t k_pair(uint32_t w, int i, uint32_t bits) {
+  return and_or(i == 0 ? w : w >> (4 * i), 0x000F000Fu, bits);
+}
+__device__ __forceinline__ uint32_t v_pair(uint32_t w, int i, uint32_t bits) {
+  return and_or(i == 0 ? w << 3 : w >> (4 * i - 3), 0x00780078u, bits);
+}
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  uint32_t y;
+  asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 constexpr float kKOffset = 128.f + 7.5f, kVOffset = 16.f + 7.5f;
 
@@ -295,6 +305,9 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) st.o[i][e] = 0.f;
 
+  const uint32_t kbits = opaque(0x43004300u), vbits = opaque(0x41804180u);
+  // units of which the query sees all: [in0, in1) of the window
+  const int in0 = (s.low + 15) >> 4, in1 = s.len >> 4;
   const int mine = u1 - u0 - warp > 0 ? (u1 - u0 - warp + kW - 1) / kW : 0;
   for (int i = 0; i < mine; ++i) {
     __syncwarp();
@@ -315,16 +328,17 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         const uint4 w0 = lds128(tb + 16 * lane), w1 = lds128(tb + 512 + 16 * lane);
         float acc[2][4];
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-          acc[gr][0] = acc[gr][2] = q0[gr][0];
-          acc[gr][1] = acc[gr][3] = q0[gr][1];
-        }
-#pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const uint32_t wa0 = word_of(w0, ks >> 1), wa1 = word_of(w1, ks >> 1);
-          const uint32_t a0 = k_pair(wa0, 2 * (ks & 1)), a1 = k_pair(wa1, 2 * (ks & 1));
-          const uint32_t a2 = k_pair(wa0, 2 * (ks & 1) + 1), a3 = k_pair(wa1, 2 * (ks & 1) + 1);
-          mma_bf16_acc(acc[ks >> 2], a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
+          const uint32_t a0 = k_pair(wa0, 2 * (ks & 1), kbits), a1 = k_pair(wa1, 2 * (ks & 1), kbits);
+          const uint32_t a2 = k_pair(wa0, 2 * (ks & 1) + 1, kbits), a3 = k_pair(wa1, 2 * (ks & 1) + 1, kbits);
+          if ((ks & 3) == 0) {  // the group's sum starts from the offset's part
+            const uint32_t af[4] = {a0, a1, a2, a3};
+            const float c0[4] = {q0[ks >> 2][0], q0[ks >> 2][1], q0[ks >> 2][0], q0[ks >> 2][1]};
+            mma_bf16(acc[ks >> 2], af, qf[ks][0], qf[ks][1], c0);
+          } else {
+            mma_bf16_acc(acc[ks >> 2], a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
+          }
           if constexpr (!PACK) mma_bf16_acc(acc[ks >> 2], a0, a1, a2, a3, qr[ks][0], qr[ks][1]);
         }
 #pragma unroll
@@ -355,21 +369,20 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
       }
     }
     // positions that the query does not see (or whose page is bad) drop out by selection
-    bool hid[KU][2];
-    bool any_hid = false;
+    uint32_t hid = 0;  // bit 2 k + rh: token r + 8 rh of tile k
+    if (bad || !((T >= in0 || 16 * (T + KU) <= s.sinks) && T + KU <= in1)) {
 #pragma unroll
-    for (int k = 0; k < KU; ++k) {
-      hid[k][0] = hid[k][1] = false;
-      if (bad || !s.whole(T + k)) {
-        any_hid = true;
+      for (int k = 0; k < KU; ++k)
 #pragma unroll
-        for (int rh = 0; rh < 2; ++rh) {
-          hid[k][rh] = bad || !s.sees(16 * (T + k) + r + 8 * rh);
+        for (int rh = 0; rh < 2; ++rh)
+          if (bad || !s.sees(16 * (T + k) + r + 8 * rh)) hid |= 1u << (2 * k + rh);
+#pragma unroll
+      for (int k = 0; k < KU; ++k)
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh)
 #pragma unroll
           for (int e = 0; e < kH; ++e)
-            if (hid[k][rh]) x[k][rh][e] = -INFINITY;
-        }
-      }
+            if ((hid >> (2 * k + rh)) & 1u) x[k][rh][e] = -INFINITY;
     }
     // running maximum; the accumulators move only when it grew a lot
     float sub[kH];
@@ -421,7 +434,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         if constexpr (INT4) {
           const uint32_t u = lds32(stage + k * kTile4Bytes + kTile4Scales + 64 + 4 * (r + 8 * rh));
           float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&u));
-          if (any_hid && hid[k][rh]) sc = make_float2(0.f, 0.f);  // a row nobody wrote may hold any scale
+          if ((hid >> (2 * k + rh)) & 1u) sc = make_float2(0.f, 0.f);  // a row nobody wrote may hold any scale
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
             const float sg = gr ? sc.y : sc.x;
@@ -449,7 +462,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t wq = word_of(w, q);
-            mma_bf16_acc(st.o[4 * gr + q], v_pair(wq, 0), v_pair(wq, 1), v_pair(wq, 2), v_pair(wq, 3), bv[gr][0], bv[gr][1]);
+            mma_bf16_acc(st.o[4 * gr + q], v_pair(wq, 0, vbits), v_pair(wq, 1, vbits), v_pair(wq, 2, vbits),
+                         v_pair(wq, 3, vbits), bv[gr][0], bv[gr][1]);
           }
         }
       } else {
