@@ -208,8 +208,9 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   constexpr int kW = R::kWarps, kS = R::kStages, KU = R::kTiles, kH = PACK ? 1 : 2;
   const WindowLaunch& a = wa.a;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ float sm_q[kMaxG * kD];
+  __shared__ __align__(16) float sm_q[kMaxG * kD];
   __shared__ float sm_ml[2][kW][kMaxG];
+  __shared__ float sm_m[kMaxG], sm_l[kMaxG];
   __shared__ int sm_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, tq = lane & 3;
   const int items = wa.items, row = blockIdx.x / items, item = blockIdx.x % items, h = blockIdx.y;
@@ -519,79 +520,85 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
       }
     }
   __syncthreads();
-  // join the warps: thread -> (head, four channels)
-  const int rec = g * (kD + 2);  // floats of a record: m[g], l[g], o[g][128]
+  // join the warps
+  if (warp == 0 && lane < g) {
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) M = fmaxf(M, sm_ml[0][w][lane]);
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      const float m = sm_ml[0][w][lane], f = m == -INFINITY ? 0.f : exp2_fast(m - M);
+      L = fmaf(sm_ml[1][w][lane], f, L);
+      sm_ml[0][w][lane] = f;
+    }
+    sm_m[lane] = M;
+    sm_l[lane] = L;
+  }
+  __syncthreads();
+  const int rec = g * (kD + 2);  // floats of a record: o[g][128], m[g], l[g]
   unsigned* counter = reinterpret_cast<unsigned*>(a.workspace) + (size_t)row * a.Hkv + h;
   float* records = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)row * a.Hkv + h) * items * rec;
-  for (int hh = warp; hh < g; hh += kW) {
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < kW; ++w) M = fmaxf(M, sm_ml[0][w][hh]);
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = 0; w < kW; ++w) {
-      const float m = sm_ml[0][w][hh];
-      if (m == -INFINITY) continue;
-      const float f = exp2_fast(m - M);
-      L = fmaf(sm_ml[1][w][hh], f, L);
-      const float4 v = reinterpret_cast<const float4*>(so + (w * g + hh) * kD)[lane];
-      y.x = fmaf(v.x, f, y.x), y.y = fmaf(v.y, f, y.y), y.z = fmaf(v.z, f, y.z), y.w = fmaf(v.w, f, y.w);
-    }
-    if (items > 1) {
-      float* rc = records + (size_t)item * rec;
-      if (lane == 0) {
-        rc[hh] = M;
-        rc[g + hh] = L;
-      }
-      float2* ro = reinterpret_cast<float2*>(rc + 2 * g + hh * kD);
-      ro[2 * lane] = make_float2(y.x, y.y);
-      ro[2 * lane + 1] = make_float2(y.z, y.w);
-    } else {
-      const float f = L > 0.f ? 1.f / L : 0.f;
-      float v[4] = {y.x * f, y.y * f, y.z * f, y.w * f};
-      if constexpr (INT4) {
-        hadamard128(v, lane);
+  for (int i = threadIdx.x; i < g * kD; i += 32 * kW) {
+    float y = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= kInvSqrt128;
+    for (int w = 0; w < kW; ++w) y = fmaf(so[w * g * kD + i], sm_ml[0][w][i >> 7], y);
+    if (items > 1)
+      records[(size_t)item * rec + i] = y;
+    else
+      sm_q[i] = y;
+  }
+  if (items > 1) {
+    if (threadIdx.x < g) {
+      records[(size_t)item * rec + g * kD + threadIdx.x] = sm_m[threadIdx.x];
+      records[(size_t)item * rec + g * kD + g + threadIdx.x] = sm_l[threadIdx.x];
+    }
+    // the last block of the (query, KV head) joins the items' records, in item order
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const unsigned t = atomicAdd(counter, 1u);
+      sm_last = t == (unsigned)items - 1u;
+      if (sm_last) *counter = 0u;
+    }
+    __syncthreads();
+    if (!sm_last) return;
+    __threadfence();
+    // a warp a head: maximum, sum and the items' factors (over the ring: every record is in the workspace)
+    float* fac = so;  // [head][items]
+    for (int hh = warp; hh < g; hh += kW) {
+      float M = -INFINITY, L = 0.f;
+      for (int i = lane; i < items; i += 32) M = fmaxf(M, __ldcg(records + (size_t)i * rec + g * kD + hh));
+      M = warp_max(M);
+      for (int i = lane; i < items; i += 32) {
+        const float m = __ldcg(records + (size_t)i * rec + g * kD + hh), f = m == -INFINITY ? 0.f : exp2_fast(m - M);
+        L = fmaf(__ldcg(records + (size_t)i * rec + g * kD + g + hh), f, L);
+        fac[hh * items + i] = f;
       }
-      uint2 u = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-      reinterpret_cast<uint2*>(a.out + ((size_t)row * a.Hq + h * g + hh) * kD)[lane] = u;
+      L = warp_sum(L);
+      if (lane == 0) sm_l[hh] = L;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < g * kD; i += 32 * kW) {
+      const float* f = fac + (i >> 7) * items;
+      float y = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < items; ++k) y = fmaf(__ldcg(records + (size_t)k * rec + i), f[k], y);
+      sm_q[i] = y;
     }
   }
-  if (items == 1) return;
-  // the last block of the (query, KV head) joins the items' records, in item order
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const unsigned t = atomicAdd(counter, 1u);
-    sm_last = t == (unsigned)items - 1u;
-    if (sm_last) *counter = 0u;
-  }
-  __syncthreads();
-  if (!sm_last) return;
-  __threadfence();
+  // normalise, turn back, round once
   for (int hh = warp; hh < g; hh += kW) {
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < items; ++i) M = fmaxf(M, __ldcg(records + (size_t)i * rec + hh));
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < items; ++i) {
-      const float* rc = records + (size_t)i * rec;
-      const float m = __ldcg(rc + hh);
-      if (m == -INFINITY) continue;
-      const float f = exp2_fast(m - M);
-      L = fmaf(__ldcg(rc + g + hh), f, L);
-      const float2* ro = reinterpret_cast<const float2*>(rc + 2 * g + hh * kD);
-      const float2 p = __ldcg(ro + 2 * lane), q = __ldcg(ro + 2 * lane + 1);
-      v[0] = fmaf(p.x, f, v[0]), v[1] = fmaf(p.y, f, v[1]), v[2] = fmaf(q.x, f, v[2]), v[3] = fmaf(q.y, f, v[3]);
-    }
-    const float f = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= f;
+    const float f = sm_l[hh] > 0.f ? 1.f / sm_l[hh] : 0.f;
+    const float4 y = reinterpret_cast<const float4*>(sm_q + hh * kD)[lane];
+    float v[4] = {y.x * f, y.y * f, y.z * f, y.w * f};
     if constexpr (INT4) {
       hadamard128(v, lane);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= kInvSqrt128;
     }
-    uint2 u = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    reinterpret_cast<uint2*>(a.out + ((size_t)row * a.Hq + h * g + hh) * kD)[lane] = u;
+    reinterpret_cast<uint2*>(a.out + ((size_t)row * a.Hq + h * g + hh) * kD)[lane] =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
 }
 

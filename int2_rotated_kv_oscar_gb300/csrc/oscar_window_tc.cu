@@ -469,22 +469,24 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
   for (int rr = warp; rr < 128 * ntile; rr += kTcwThreads / 32) {
     const int tt = rr >> 7, r = rr & 127, q = i0 + tt * qpt + r / g;
     if (r >= qpt * g || q >= n) continue;
+    // lane i holds item i's maximum and sum (items <= 2 SMs: the lanes go round)
     float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < ta.items; ++i) M = fmaxf(M, __ldcg(recs + ((size_t)i * 256 + rr) * kRowFloats + kD));
-    float2 y0 = make_float2(0.f, 0.f), y1 = make_float2(0.f, 0.f);
+    for (int i = lane; i < ta.items; i += 32) M = fmaxf(M, __ldcg(recs + ((size_t)i * 256 + rr) * kRowFloats + kD));
+    M = warp_max(M);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int i = 0; i < ta.items; ++i) {
       const float* rec = recs + ((size_t)i * 256 + rr) * kRowFloats;
-      const float mi = __ldcg(rec + kD);
-      if (mi == -INFINITY) continue;
-      const float f = exp2_t((mi - M) * c);
+      const float mi = __ldcg(rec + kD), f = mi == -INFINITY ? 0.f : exp2_t((mi - M) * c);
       L = fmaf(__ldcg(rec + kD + 1), f, L);
-      const float2 u = __ldcg(reinterpret_cast<const float2*>(rec) + 2 * lane), v = __ldcg(reinterpret_cast<const float2*>(rec) + 2 * lane + 1);
-      y0 = ffma2(u, make_float2(f, f), y0);
-      y1 = ffma2(v, make_float2(f, f), y1);
+      // (an item without keys wrote m and l = 0 alone)
+      const float2 u = __ldcg(reinterpret_cast<const float2*>(rec) + 2 * lane);
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(rec) + 2 * lane + 1);
+      if (f > 0.f) y = make_float4(fmaf(u.x, f, y.x), fmaf(u.y, f, y.y), fmaf(v.x, f, y.z), fmaf(v.y, f, y.w));
     }
     const float f = L > 0.f ? 1.f / L : 0.f;
     reinterpret_cast<uint2*>(a.out + ((size_t)(row0 + q) * a.Hq + h * g + r % g) * kD)[lane] =
-        make_uint2(pack_bf16x2(y0.x * f, y0.y * f), pack_bf16x2(y1.x * f, y1.y * f));
+        make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
   }
 }
 
