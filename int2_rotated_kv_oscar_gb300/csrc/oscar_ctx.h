@@ -3,7 +3,7 @@
 
 #include <vector>
 
-#include "../../include/oscar.h"
+#include "oscar.h"
 #include "oscar_internal.h"
 
 struct oscar_ctx {

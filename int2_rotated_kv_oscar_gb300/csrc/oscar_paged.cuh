@@ -86,5 +86,24 @@ __device__ __forceinline__ void load4(float* v, const float* p) {
 
 __device__ __forceinline__ int odd_bits(int x) { return __popc((unsigned)x) & 1; }
 
+// Two bf16 signs: +-1 with the low half's sign bit lo and the high half's hi.
+__device__ __forceinline__ uint32_t signs_bf16(int lo, int hi) {
+  return 0x3F803F80u ^ ((uint32_t)lo << 15) ^ ((uint32_t)hi << 31);
+}
+
+// The add/subtract stages over bits 2, 5, 6: d[2 M + b2] is combination (M = bits 5, 6; b2 = bit 2).
+template <int N>
+__device__ __forceinline__ void butterfly(float2 (&d)[8][N], int stage) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (!(i & stage))
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float2 x = d[i][j], y = d[i | stage][j];
+        d[i][j] = fadd2(x, y);
+        d[i | stage][j] = ffma2(y, make_float2(-1.f, -1.f), x);
+      }
+}
+
 }  // namespace
 }  // namespace oscar

@@ -56,10 +56,9 @@ struct Read4Launch {
 };
 cudaError_t launch_int4_to_bf16(const Read4Launch& a, cudaStream_t stream);
 
-// How the attention's split over the keys is laid out (one query and KV head's
-// visible keys are cut into `items` work items, one block each).
+// How the attention's work is laid out over blocks.
 struct WindowPlan {
-  int32_t items = 1;
+  int32_t items = 1;  // split kernel: blocks; tensor-core kernel: blocks that share one (tile pair, KV head)
   size_t off_records = 0, total = 0;  // workspace: counters, then the items' records; one size for all calls
 };
 

@@ -125,7 +125,7 @@ oscar_status window_launch(const oscar_ctx* ctx, const oscar_window_args* args, 
                 : plan_window(int4, args->n_tokens, a->Hq, a->Hkv, keys, ctx->num_sms);
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < oscar_window_workspace_bytes(ctx)) return OSCAR_ERR_WORKSPACE;
   a->workspace = static_cast<uint8_t*>(ws);
-  if ((int64_t)args->n_tokens * a->plan.items > INT32_MAX) return OSCAR_ERR_UNSUPPORTED;
+  if ((int64_t)args->n_tokens * a->Hkv > INT32_MAX) return OSCAR_ERR_UNSUPPORTED;
   return OSCAR_OK;
 }
 

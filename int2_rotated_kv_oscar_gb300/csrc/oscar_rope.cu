@@ -149,20 +149,6 @@ __device__ __forceinline__ void turn_tile(Tile4& t, const RopeLaunch& a, int p_r
   }
 }
 
-// The add/subtract stages over bits 2, 5, 6: d[2 M + b2] is combination (M = bits 5, 6; b2 = bit 2).
-template <int N>
-__device__ __forceinline__ void butterfly(float2 (&d)[8][N], int stage) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (!(i & stage))
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float2 x = d[i][j], y = d[i | stage][j];
-        d[i][j] = fadd2(x, y);
-        d[i | stage][j] = ffma2(y, make_float2(-1.f, -1.f), x);
-      }
-}
-
 constexpr float kMaxScale4 = 65504.0f;           // fp16's largest, the scale of a group that overflows it
 constexpr float kMagic4 = 12582912.0f + 8.0f;    // 1.5 2^23 + 8: the sum's low bits are floor(x' / s) + 8
 constexpr uint32_t kMagic4Bits = 0x4B400000u;
@@ -232,11 +218,6 @@ __device__ __forceinline__ void pack_v(const float2 (&d)[8][4], const float2 (&i
 
 __device__ __forceinline__ float max4(float m, float2 a, float2 b) {
   return fmaxf(fmaxf(m, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
-}
-
-// Two bf16 signs: +-1 with the low half's sign bit lo and the high half's hi.
-__device__ __forceinline__ uint32_t signs_bf16(int lo, int hi) {
-  return 0x3F803F80u ^ ((uint32_t)lo << 15) ^ ((uint32_t)hi << 31);
 }
 
 template <int TURN>

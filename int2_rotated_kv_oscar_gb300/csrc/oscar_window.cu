@@ -3,13 +3,16 @@
 // 4-bit cache.
 //
 // One (query, KV head) sees a list of 16-token tiles: those of the sinks, then
-// those of the window.  The list is cut into work items, one block each; the
-// warps of a block take units of it (one tile of BF16 rows, two tiles of the
-// 4-bit cache) in turn, each with a ring of units copied ahead by cp.async and
-// an online softmax of its own (running maximum m, sum l, accumulator o, all
-// fp32, base-2 exponents).  The block joins its warps' states; when there are
-// several items, the last block to finish joins their records in item order,
-// so the result does not depend on which one that is.
+// those of the window, in units of one tile (BF16) or two (4 bits).  The units
+// of all (query, KV head) pairs, one pair after another, are cut into one equal
+// range for each block (every block adds up the rows' lengths for itself), so
+// that ragged lengths leave no SM idle; a range holds one or more segments of
+// pairs.  The warps of a block take a segment's units in turn, each with a ring
+// of units copied ahead by cp.async and an online softmax of its own (running
+// maximum m, sum l, accumulator o, all fp32, base-2 exponents).  The block
+// joins its warps' states; a pair that is cut leaves a record of each segment,
+// and the last block to finish joins them in block order, so the result does
+// not depend on which one that is.
 //
 // Products run on m16n8k16 MMAs with the cached side as the 16 rows (tokens in
 // Q K, channels in P V) and the g query heads of a KV head as the 8 columns.
@@ -31,12 +34,14 @@ constexpr float kLazyW = 8.0f;  // the accumulators are rescaled when the maximu
 template <bool INT4>
 struct Ring {
   static constexpr int kWarps = INT4 ? 16 : 8;
+  static constexpr int kBlocks = 1;                       // blocks per SM
   static constexpr int kTiles = INT4 ? 2 : 1;                        // 16-token tiles of a unit
   static constexpr int kUnit = INT4 ? 2 * kTile4Bytes : 16 * kD * 4;  // bytes of a unit
   static constexpr int kStages = 3;
   static constexpr int kBytes = kWarps * kStages * kUnit;
 };
-constexpr int kSplitBlocks = 4;  // blocks per SM that one call may split its keys over
+constexpr int kSlack = 8;
+constexpr int kMaxRows = 1024;  // query rows whose lengths a block adds up; with more, a block takes one whole pair
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
   const unsigned n = real ? 16u : 0u;
@@ -135,7 +140,7 @@ __device__ __forceinline__ bool seen_by(const WindowLaunch& a, int i, int& b, Se
 
 struct WindowArgs {
   WindowLaunch a;
-  int items;
+  bool cut;  // the pairs' units are cut into equal ranges (else a block a pair)
 };
 
 // Copy unit `t0` (tile index in the list) of the query's keys into a stage.  BF16: rows of 256 bytes,
@@ -174,27 +179,44 @@ struct State {
   float o[8][4];
 };
 
-// 4-bit words to bf16 pairs, from the bits alone.  K: 128 + c.  V: 16 + c: a smaller offset, because P V
-// cancels it against the sum of the weights and the MMA's fp32 sums truncate relative to it (the logits'
-// offset is cancelled inside one tile's product).  The exponent bits come in a register, so that masking
-// and setting them is one LOP3 (as two constants they were two: 64 of 370 instructions a tile).
+// 4-bit words to pairs of 16-bit floats, from the bits alone: a nibble in the mantissa under a fixed exponent.
+// K (fp16): the word two bits up and six down has its pairs at bits 2 and 6, where they read 256 + c and
+// 16 + c: two shifts and four LOP3 a word.  V (bf16, for the range of the weights): every pair at bit 3, 16 + c:
+// P V cancels the offset against the sum of the weights over all keys, and the MMA's fp32 sums truncate
+// relative to it, so it is kept small (the logits' offset is cancelled inside one tile's product).  The
+// exponent bits come in a register, so that masking and setting them is one LOP3 (as two constants they were two:
+// 64 of 370 instructions a tile).
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
   uint32_t y;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
   return y;
 }
-__device__ __forceinline__ uint32_t k_pair(uint32_t w, int i, uint32_t bits) {
-  return and_or(i == 0 ? w : w >> (4 * i), 0x000F000Fu, bits);
+struct KBits {
+  uint32_t b256, b16;
+};
+// pairs (2 b2, 2 b2 + 1) of a word: channel bit 1 = 0 as 256 + c, = 1 as 16 + c
+__device__ __forceinline__ void k_pairs(uint32_t w, int b2, const KBits& k, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x = b2 == 0 ? w << 2 : w >> 6;
+  lo = and_or(x, 0x003C003Cu, k.b256);
+  hi = and_or(x, 0x03C003C0u, k.b16);
 }
 __device__ __forceinline__ uint32_t v_pair(uint32_t w, int i, uint32_t bits) {
   return and_or(i == 0 ? w << 3 : w >> (4 * i - 3), 0x00780078u, bits);
+}
+// D = A B + C, m16n8k16, fp16 operands, fp32 sums
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1, const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ uint32_t opaque(uint32_t x) {
   uint32_t y;
   asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-constexpr float kKOffset = 128.f + 7.5f, kVOffset = 16.f + 7.5f;
+constexpr float kKOffset0 = 256.f + 7.5f, kKOffset1 = 16.f + 7.5f, kVOffset = 16.f + 7.5f;
 
 // value + residual of x as a bf16 pair (value in the low half)
 __device__ __forceinline__ uint32_t split_bf16(float x) {
@@ -213,14 +235,129 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   __shared__ float sm_m[kMaxG], sm_l[kMaxG];
   __shared__ int sm_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, tq = lane & 3;
-  const int items = wa.items, row = blockIdx.x / items, item = blockIdx.x % items, h = blockIdx.y;
-  const int g = a.Hq / a.Hkv;
-  int b;
+  __shared__ int pre[kMaxRows + 1], scan[kW];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int g = a.Hq / a.Hkv, rows = a.tok.n_tokens, G = gridDim.x, block = blockIdx.x;
+  const bool few = rows <= 32;  // each warp adds the rows up for itself, lane i row i
+  int at = 0, end = 1, total = 0;  // this block's range of all units
+  int pre_l = 0, units_l = 0;                // few: units before row `lane` (of one KV head), and its own
+  if (wa.cut) {
+    int b;
+    Seen s;
+    if (few) {
+      if (lane < rows && seen_by<KU>(a, lane, b, s, block == 0 && warp == 0)) units_l = s.tiles() / KU;
+      pre_l = units_l;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, pre_l, o);
+        if (lane >= o) pre_l += y;
+      }
+      total = __shfl_sync(0xffffffffu, pre_l, 31);
+      pre_l -= units_l;
+    } else {
+      // pre[i]: units of the rows before row i
+      constexpr int kPer = kMaxRows / (32 * kW);
+      const int per = (rows + 32 * kW - 1) / (32 * kW), first = threadIdx.x * per;
+      int n[kPer], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        n[i] = 0;
+        if (i < per && first + i < rows && seen_by<KU>(a, first + i, b, s, block == 0)) n[i] = s.tiles() / KU;
+        sum += n[i];
+      }
+      int inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) scan[warp] = inc;
+      __syncthreads();
+      int before = inc - sum;
+      for (int w = 0; w < warp; ++w) before += scan[w];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < per && first + i < rows) {
+          pre[first + i] = before;
+          before += n[i];
+          if (first + i == rows - 1) pre[rows] = before;
+        }
+      __syncthreads();
+      total = pre[rows];
+    }
+    total *= a.Hkv;
+    // queries that see nothing get zeros
+    for (int i = block; i < rows; i += G) {
+      const int n = few ? __shfl_sync(0xffffffffu, units_l, i) : pre[i + 1] - pre[i];
+      if (n == 0 && seen_by<KU>(a, i, b, s, false))
+        for (int c = threadIdx.x; c < a.Hq * (kD / 8); c += 32 * kW)
+          reinterpret_cast<uint4*>(a.out + (size_t)i * a.Hq * kD)[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  // the pair that unit x belongs to: its row, KV head, first unit and units
+  auto pair_of = [&](int x, int& row, int& h, int& units) {
+    int before;
+    if (few) {
+      row = __ffs(__ballot_sync(0xffffffffu, pre_l * a.Hkv <= x && x < (pre_l + units_l) * a.Hkv)) - 1;
+      before = __shfl_sync(0xffffffffu, pre_l, row);
+      units = __shfl_sync(0xffffffffu, units_l, row);
+    } else {
+      int hi_r = rows;
+      row = 0;  // the last row whose units start at or before x (rows without units share their successor's start)
+      while (hi_r - row > 1) {
+        const int mid = (row + hi_r) >> 1;
+        if (pre[mid] * a.Hkv <= x)
+          row = mid;
+        else
+          hi_r = mid;
+      }
+      before = pre[row];
+      units = pre[row + 1] - before;
+    }
+    const int in = x - before * a.Hkv;
+    h = (int)__fdividef((float)in, (float)units);  // within one of the quotient, as long as it is below 2^20
+    h += (h + 1) * units <= in ? 1 : h * units > in ? -1 : 0;
+    return before * a.Hkv + h * units;
+  };
+  // where block k's range begins: near the k-th of G equal parts (a product of floats: the same everywhere and
+  // monotonic in k, which is all that matters), or at the pair's edge when that is at most kSlack units away (a
+  // segment costs as much as several units of every warp)
+  const float step = (float)total / (float)G;
+  auto begin_of = [&](int k) {
+    const int x = k >= G ? total : min(total, (int)(step * (float)k));
+    if (x == 0 || x >= total) return x;
+    int row, h, units;
+    const int p = pair_of(x, row, h, units);
+    return x - p <= kSlack && x - p < units ? p : p + units - x <= kSlack ? p + units : x;
+  };
+  auto block_of = [&](int x) {  // the block whose range holds unit x
+    int k = min(G - 1, (int)__fdividef((float)x, step));
+    while (begin_of(k) > x) --k;
+    while (begin_of(k + 1) <= x) ++k;
+    return k;
+  };
+  if (wa.cut) {
+    at = begin_of(block);
+    end = begin_of(block + 1);
+  }
+  for (bool again = false; at < end; again = true) {
+  if (again) __syncthreads();  // the segment before is done with shared memory
+  int row, h, u0 = 0, u1, units, b;
   Seen s;
-  if (!seen_by<KU>(a, row, b, s, threadIdx.x == 0 && item == 0 && h == 0)) return;
-  // this item's units [u0, u1), this warp's: u0 + warp, + kW, ...
-  const int units = s.tiles() / KU;
-  const int u0 = (int)((long long)units * item / items), u1 = (int)((long long)units * (item + 1) / items);
+  if (wa.cut) {
+    u0 = at - pair_of(at, row, h, units);
+    u1 = min(units, u0 + (end - at));
+    seen_by<KU>(a, row, b, s, false);
+  } else {
+    row = block / a.Hkv;
+    h = block % a.Hkv;
+    if (!seen_by<KU>(a, row, b, s, h == 0 && threadIdx.x == 0)) return;
+    u1 = units = s.tiles() / KU;
+  }
+  // this segment's units [u0, u1), this warp's: u0 + warp, + kW, ...
+  const int pair0 = at - u0;  // the pair's first unit among all
+  at += wa.cut ? u1 - u0 : 1;
   const uint32_t ring = smem_u32(sm) + warp * (kS * R::kUnit);
   int phys_l = -1, fetched = 0;  // lane i: the page of the warp's unit fetched - 32 + i
   auto issue = [&](int i) {      // the warp's i-th unit
@@ -236,53 +373,74 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     cp_async_commit();
     return phys;
   };
+  const uint16_t* qrow = a.q + (size_t)row * a.q_stride + (size_t)h * g * kD;
+  uint4 qx[4];  // 4 bits: pieces tq + 4 M of the column's query (loaded before the copies wait for their pages)
+  if constexpr (INT4) {
+    const int hh = PACK ? r >> 1 : r;
+#pragma unroll
+    for (int M = 0; M < 4; ++M)
+      qx[M] = hh < g ? reinterpret_cast<const uint4*>(qrow + hh * kD)[tq + 4 * M] : make_uint4(0u, 0u, 0u, 0u);
+  }
   int phys_q[kS];
 #pragma unroll
   for (int i = 0; i < kS - 1; ++i) phys_q[i] = issue(i);
 
   // the queries as MMA columns: qf[k step][2], and the offset's part of the logits
-  uint32_t qf[8][2], qr[8][2];
-  float q0[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // [group][column of the lane's two]
-  const uint16_t* qrow = a.q + (size_t)row * a.q_stride + (size_t)h * g * kD;
+  uint32_t qf[8][2];
+  float q0[2][4];  // 4 bits: [group] the offset's part of a tile's logits, as the MMA's C
+  float qscale[kH];  // logits to base-2 exponents, by the lane's heads
   if constexpr (INT4) {
-    for (int hh = warp; hh < kMaxG; hh += kW) {
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (hh < g) {
-        const uint2 u = *reinterpret_cast<const uint2*>(qrow + hh * kD + 4 * lane);
-        v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-        hadamard128(v, lane);
-      }
-      const float f = kInvSqrt128 * a.sm_scale * kLog2eW;
+    // q H / sqrt(128) as the append turns K: column r's head is row r of the MMAs, so that the lane ends up
+    // with the channels of its column's fragments (k step 2 M + b2: k bits e, tq, kh = channel bits 0, (3, 4), 1)
+    const uint32_t s1 = signs_bf16(odd_bits(2 * tq & r), odd_bits((2 * tq + 1) & r));
+    float2 d[8][2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sm_q[hh * kD + 4 * lane + e] = v[e] * f;
-    }
-    __syncthreads();
-    // k step 2 M + b2: k bits e, tq, kh = channel bits 0, (3, 4), 1; bits 2, 5, 6 = b2, M
-    const int hh = PACK ? r >> 1 : r;
-    const bool live = hh < g;
-    float part[2] = {0.f, 0.f}, partr[2] = {0.f, 0.f};
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_bf16_acc(acc, word_of(qx[i >> 1], 2 * (i & 1)), 0u, word_of(qx[i >> 1], 2 * (i & 1) + 1), 0u, s1,
+                     nt ? s1 ^ 0x80008000u : s1);
+        d[i][nt] = make_float2(acc[0], acc[1]);
+      }
+    butterfly(d, 1);
+    butterfly(d, 2);
+    butterfly(d, 4);
+    // fp16 with a power of two taken out (the largest channel becomes 8..16); PACK: value and residual (2^-22),
+    // else the value alone (2^-11 of a channel's part of the logit)
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) top = fmaxf(top, fmaxf(fabsf(d[i][nt].x), fabsf(d[i][nt].y)));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^(3 - floor(log2 top)) and its inverse, from the exponent bits (kept where both are normal)
+    const int ex = min(max((int)(__float_as_uint(top) >> 23), 8), 250);
+    const float up = __uint_as_float((uint32_t)(127 + 3 - (ex - 127)) << 23), down = __uint_as_float((uint32_t)(ex - 3) << 23);
+    float part[2] = {0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
       for (int kh = 0; kh < 2; ++kh) {
-        const int j = 32 * (ks >> 1) + 8 * tq + 4 * (ks & 1) + 2 * kh;
-        const float x0 = live ? sm_q[hh * kD + j] : 0.f, x1 = live ? sm_q[hh * kD + j + 1] : 0.f;
-        const uint32_t v = pack_bf16x2(x0, x1);
-        const uint32_t res = pack_bf16x2(x0 - bf16_lo(v), x1 - bf16_hi(v));
-        qf[ks][kh] = PACK && (r & 1) ? res : v;
-        qr[ks][kh] = res;
-        part[ks >> 2] += bf16_lo(qf[ks][kh]) + bf16_hi(qf[ks][kh]);
-        partr[ks >> 2] += bf16_lo(res) + bf16_hi(res);
+        const float x0 = d[ks][kh].x * up, x1 = d[ks][kh].y * up;
+        __half2 v = __floats2half2_rn(x0, x1);
+        if (PACK && (r & 1)) v = __floats2half2_rn(x0 - __low2float(v), x1 - __high2float(v));
+        qf[ks][kh] = h2_as_u32(v);
+        part[ks >> 2] = fmaf(kh ? -kKOffset1 : -kKOffset0, __low2float(v) + __high2float(v), part[ks >> 2]);
       }
     // sums over the column's four lanes, then to the lanes that hold columns 2 tq, 2 tq + 1 of the logits
 #pragma unroll
     for (int gr = 0; gr < 2; ++gr) {
-      float x = PACK ? part[gr] : part[gr] + partr[gr];
+      float x = part[gr];
       x += __shfl_xor_sync(0xffffffffu, x, 1);
       x += __shfl_xor_sync(0xffffffffu, x, 2);
-      q0[gr][0] = -kKOffset * __shfl_sync(0xffffffffu, x, 4 * (2 * tq));
-      q0[gr][1] = -kKOffset * __shfl_sync(0xffffffffu, x, 4 * (2 * tq + 1));
+      q0[gr][0] = q0[gr][2] = __shfl_sync(0xffffffffu, x, 4 * (2 * tq));
+      q0[gr][1] = q0[gr][3] = __shfl_sync(0xffffffffu, x, 4 * (2 * tq + 1));
     }
+    const float f = down * (kInvSqrt128 * a.sm_scale * kLog2eW);
+    qscale[0] = __shfl_sync(0xffffffffu, f, 4 * (2 * tq));
+    qscale[kH - 1] = PACK ? qscale[0] : __shfl_sync(0xffffffffu, f, 4 * (2 * tq + 1));
   } else {
     const int hh = PACK ? r >> 1 : r;
     const bool live = hh < g && !(PACK && (r & 1));  // a bf16 query has no residual
@@ -291,8 +449,11 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
       qf[ks][0] = live ? *reinterpret_cast<const uint32_t*>(qrow + hh * kD + 16 * ks + 2 * tq) : 0u;
       qf[ks][1] = live ? *reinterpret_cast<const uint32_t*>(qrow + hh * kD + 16 * ks + 8 + 2 * tq) : 0u;
     }
+    qscale[0] = qscale[kH - 1] = a.sm_scale * kLog2eW;
   }
-  const float qscale = INT4 ? 1.f : a.sm_scale * kLog2eW;
+  const bool split = u0 > 0 || u1 < units;
+  const int kf = split ? block_of(pair0) : block;  // the blocks that hold the pair's units
+  const int pieces = split ? block_of(pair0 + units - 1) - kf + 1 : 1;
 
   State<PACK, INT4> st;
 #pragma unroll
@@ -306,7 +467,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) st.o[i][e] = 0.f;
 
-  const uint32_t kbits = opaque(0x43004300u), vbits = opaque(0x41804180u);
+  const KBits kbits = {opaque(0x5C005C00u), opaque(0x4C004C00u)};
+  const uint32_t vbits = opaque(0x41804180u);
   // units of which the query sees all: [in0, in1) of the window
   const int in0 = (s.low + 15) >> 4, in1 = s.len >> 4;
   const int mine = u1 - u0 - warp > 0 ? (u1 - u0 - warp + kW - 1) / kW : 0;
@@ -320,7 +482,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     const bool bad = phys_q[0] < 0;
 #pragma unroll
     for (int j = 0; j < kS - 1; ++j) phys_q[j] = phys_q[j + 1];
-    // logits x[tile][row half][head], base 2
+    // logits x[tile][row half][head]; x qscale is the base-2 exponent
     float x[KU][2][kH];
 #pragma unroll
     for (int k = 0; k < KU; ++k) {
@@ -330,17 +492,13 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         float acc[2][4];
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t wa0 = word_of(w0, ks >> 1), wa1 = word_of(w1, ks >> 1);
-          const uint32_t a0 = k_pair(wa0, 2 * (ks & 1), kbits), a1 = k_pair(wa1, 2 * (ks & 1), kbits);
-          const uint32_t a2 = k_pair(wa0, 2 * (ks & 1) + 1, kbits), a3 = k_pair(wa1, 2 * (ks & 1) + 1, kbits);
-          if ((ks & 3) == 0) {  // the group's sum starts from the offset's part
-            const uint32_t af[4] = {a0, a1, a2, a3};
-            const float c0[4] = {q0[ks >> 2][0], q0[ks >> 2][1], q0[ks >> 2][0], q0[ks >> 2][1]};
-            mma_bf16(acc[ks >> 2], af, qf[ks][0], qf[ks][1], c0);
-          } else {
-            mma_bf16_acc(acc[ks >> 2], a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
-          }
-          if constexpr (!PACK) mma_bf16_acc(acc[ks >> 2], a0, a1, a2, a3, qr[ks][0], qr[ks][1]);
+          uint32_t a0, a1, a2, a3;
+          k_pairs(word_of(w0, ks >> 1), ks & 1, kbits, a0, a2);
+          k_pairs(word_of(w1, ks >> 1), ks & 1, kbits, a1, a3);
+          if ((ks & 3) == 0)  // the group's sum starts from the offset's part
+            mma_f16_from(acc[ks >> 2], a0, a1, a2, a3, qf[ks][0], qf[ks][1], q0[ks >> 2]);
+          else
+            mma_f16(acc[ks >> 2], a0, a1, a2, a3, qf[ks][0], qf[ks][1]);
         }
 #pragma unroll
         for (int rh = 0; rh < 2; ++rh) {
@@ -364,8 +522,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         }
 #pragma unroll
         for (int rh = 0; rh < 2; ++rh) {
-          x[k][rh][0] = acc[2 * rh] * qscale;
-          if constexpr (!PACK) x[k][rh][kH - 1] = acc[2 * rh + 1] * qscale;
+          x[k][rh][0] = acc[2 * rh];
+          if constexpr (!PACK) x[k][rh][kH - 1] = acc[2 * rh + 1];
         }
       }
     }
@@ -401,13 +559,13 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     }
     bool grow = false;
 #pragma unroll
-    for (int e = 0; e < kH; ++e) grow = grow || sub[e] > st.m[e] + kLazyW || (st.m[e] == -INFINITY && sub[e] > -INFINITY);
+    for (int e = 0; e < kH; ++e) grow = grow || (sub[e] - st.m[e]) * qscale[e] > kLazyW || (st.m[e] == -INFINITY && sub[e] > -INFINITY);
     if (__any_sync(0xffffffffu, grow)) {
       float f[kH];
 #pragma unroll
       for (int e = 0; e < kH; ++e) {
         const float m = fmaxf(st.m[e], sub[e]);
-        f[e] = st.m[e] == -INFINITY ? 0.f : exp2_fast(st.m[e] - m);
+        f[e] = st.m[e] == -INFINITY ? 0.f : exp2_fast((st.m[e] - m) * qscale[e]);
         st.m[e] = m;
         st.l[e] *= f[e];
         st.wsum[e][0] *= f[e];
@@ -419,7 +577,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         for (int e = 0; e < 4; ++e) st.o[mt][e] *= PACK ? f[0] : f[(e & 1) * (kH - 1)];
     }
 #pragma unroll
-    for (int e = 0; e < kH; ++e) sub[e] = st.m[e] == -INFINITY ? 0.f : st.m[e];
+    for (int e = 0; e < kH; ++e) sub[e] = st.m[e] == -INFINITY ? 0.f : -st.m[e] * qscale[e];
 #pragma unroll
     for (int k = 0; k < KU; ++k) {
       // weights, as the MMA's columns: transposed 8 x 8 blocks (tokens 0-7 and 8-15)
@@ -429,7 +587,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         float p[kH];
 #pragma unroll
         for (int e = 0; e < kH; ++e) {
-          p[e] = exp2_fast(x[k][rh][e] - sub[e]);
+          p[e] = exp2_fast(fmaf(x[k][rh][e], qscale[e], sub[e]));
           st.l[e] += p[e];
         }
         if constexpr (INT4) {
@@ -496,7 +654,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
     for (int e = 0; e < kH; ++e) {
       const int hh = PACK ? tq : 2 * tq + e;
-      sm_ml[0][warp][hh] = st.m[e];
+      sm_ml[0][warp][hh] = st.m[e] * qscale[e];  // (a base-2 exponent from here on)
       sm_ml[1][warp][hh] = st.l[e];
     }
 #pragma unroll
@@ -535,55 +693,92 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     sm_l[lane] = L;
   }
   __syncthreads();
-  const int rec = g * (kD + 2);  // floats of a record: o[g][128], m[g], l[g]
-  unsigned* counter = reinterpret_cast<unsigned*>(a.workspace) + (size_t)row * a.Hkv + h;
-  float* records = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)row * a.Hkv + h) * items * rec;
+  const int rec = (g * (kD + 2) + 3) & ~3;  // floats of a record: o[g][128], m[g], l[g]
+  // block k's records: 2 k (a pair that began in an earlier block), 2 k + 1 (a pair that goes on in the next)
+  float* records = reinterpret_cast<float*>(a.workspace + a.plan.off_records);
+  float* mine_rec = records + (size_t)(2 * block + (block == kf)) * rec;
   for (int i = threadIdx.x; i < g * kD; i += 32 * kW) {
     float y = 0.f;
 #pragma unroll
     for (int w = 0; w < kW; ++w) y = fmaf(so[w * g * kD + i], sm_ml[0][w][i >> 7], y);
-    if (items > 1)
-      records[(size_t)item * rec + i] = y;
+    if (split)
+      mine_rec[i] = y;
     else
       sm_q[i] = y;
   }
-  if (items > 1) {
+  if (split) {
     if (threadIdx.x < g) {
-      records[(size_t)item * rec + g * kD + threadIdx.x] = sm_m[threadIdx.x];
-      records[(size_t)item * rec + g * kD + g + threadIdx.x] = sm_l[threadIdx.x];
+      mine_rec[g * kD + threadIdx.x] = sm_m[threadIdx.x];
+      mine_rec[g * kD + g + threadIdx.x] = sm_l[threadIdx.x];
     }
-    // the last block of the (query, KV head) joins the items' records, in item order
-    __threadfence();
+    // the last block of the pair joins the pieces' records, in block order
     __syncthreads();
     if (threadIdx.x == 0) {
-      const unsigned t = atomicAdd(counter, 1u);
-      sm_last = t == (unsigned)items - 1u;
+      // releases the block's records (the barrier put them before it) and acquires the other blocks'
+      unsigned* counter = reinterpret_cast<unsigned*>(a.workspace) + kf;  // one pair at most goes on from block kf
+      unsigned t;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(t) : "l"(counter) : "memory");
+      sm_last = t == (unsigned)pieces - 1u;
       if (sm_last) *counter = 0u;
     }
     __syncthreads();
-    if (!sm_last) return;
-    __threadfence();
-    // a warp a head: maximum, sum and the items' factors (over the ring: every record is in the workspace)
-    float* fac = so;  // [head][items]
+    if (!sm_last) continue;
+    auto piece = [&](int i) { return records + (size_t)(2 * (kf + i) + (i == 0)) * rec; };
+    // thread -> (four channels of a head, every kParts-th piece): its loads go out before the factors are known
+    constexpr int kCells = (PACK ? 4 : 8) * (kD / 4), kParts = 32 * kW / kCells, kAhead = 8;
+    const int cell = threadIdx.x % kCells, part = threadIdx.x / kCells, ch = cell / (kD / 4);
+    float4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int k = part + i * kParts;
+      v[i] = k < pieces && ch < g ? __ldcg(reinterpret_cast<const float4*>(piece(k)) + cell) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // a warp a head: maximum, sum and the pieces' factors (over the ring: every record is in the workspace)
+    float* fac = so;  // [head][pieces], then the parts' sums [part][cell]
+    float4* sums = reinterpret_cast<float4*>(so + kMaxG * G);
     for (int hh = warp; hh < g; hh += kW) {
-      float M = -INFINITY, L = 0.f;
-      for (int i = lane; i < items; i += 32) M = fmaxf(M, __ldcg(records + (size_t)i * rec + g * kD + hh));
+      float M = -INFINITY, L = 0.f, m0 = -INFINITY, l0 = 0.f;
+      if (lane < pieces) {
+        m0 = __ldcg(piece(lane) + g * kD + hh);
+        l0 = __ldcg(piece(lane) + g * kD + g + hh);
+      }
+      M = m0;
+      for (int i = lane + 32; i < pieces; i += 32) M = fmaxf(M, __ldcg(piece(i) + g * kD + hh));
       M = warp_max(M);
-      for (int i = lane; i < items; i += 32) {
-        const float m = __ldcg(records + (size_t)i * rec + g * kD + hh), f = m == -INFINITY ? 0.f : exp2_fast(m - M);
-        L = fmaf(__ldcg(records + (size_t)i * rec + g * kD + g + hh), f, L);
-        fac[hh * items + i] = f;
+      for (int i = lane; i < pieces; i += 32) {
+        const float m = i < 32 ? m0 : __ldcg(piece(i) + g * kD + hh), f = m == -INFINITY ? 0.f : exp2_fast(m - M);
+        L = fmaf(i < 32 ? l0 : __ldcg(piece(i) + g * kD + g + hh), f, L);
+        fac[hh * pieces + i] = f;
       }
       L = warp_sum(L);
       if (lane == 0) sm_l[hh] = L;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < g * kD; i += 32 * kW) {
-      const float* f = fac + (i >> 7) * items;
-      float y = 0.f;
-#pragma unroll 8
-      for (int k = 0; k < items; ++k) y = fmaf(__ldcg(records + (size_t)k * rec + i), f[k], y);
-      sm_q[i] = y;
+    if (ch < g) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = part + i * kParts;
+        const float f = k < pieces ? fac[ch * pieces + k] : 0.f;
+        y = make_float4(fmaf(v[i].x, f, y.x), fmaf(v[i].y, f, y.y), fmaf(v[i].z, f, y.z), fmaf(v[i].w, f, y.w));
+      }
+#pragma unroll 4
+      for (int k = part + kAhead * kParts; k < pieces; k += kParts) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(piece(k)) + cell);
+        const float f = fac[ch * pieces + k];
+        y = make_float4(fmaf(u.x, f, y.x), fmaf(u.y, f, y.y), fmaf(u.z, f, y.z), fmaf(u.w, f, y.w));
+      }
+      sums[part * kCells + cell] = y;
+    }
+    __syncthreads();
+    if (part == 0 && ch < g) {
+      float4 y = sums[cell];
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) {
+        const float4 u = sums[i * kCells + cell];
+        y = make_float4(y.x + u.x, y.y + u.y, y.z + u.z, y.w + u.w);
+      }
+      reinterpret_cast<float4*>(sm_q)[cell] = y;
     }
   }
   __syncthreads();
@@ -600,10 +795,11 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     reinterpret_cast<uint2*>(a.out + ((size_t)row * a.Hq + h * g + hh) * kD)[lane] =
         make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
+  }
 }
 
 template <bool PACK, bool INT4>
-__global__ void __launch_bounds__(32 * Ring<INT4>::kWarps, 1) window_split_kernel(const __grid_constant__ WindowArgs wa) {
+__global__ void __launch_bounds__(32 * Ring<INT4>::kWarps, Ring<INT4>::kBlocks) window_split_kernel(const __grid_constant__ WindowArgs wa) {
   window_body<PACK, INT4>(wa);
 }
 
@@ -617,35 +813,29 @@ cudaError_t launch_one(const WindowLaunch& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   WindowArgs wa;
   wa.a = a;
-  wa.items = a.plan.items;
-  window_split_kernel<PACK, INT4>
-      <<<dim3((unsigned)(a.tok.n_tokens * (long long)wa.items), a.Hkv), 32 * Ring<INT4>::kWarps, smem, stream>>>(wa);
-  return cudaGetLastError();
+  wa.cut = a.plan.items > 0;
+  const long long blocks = wa.cut ? a.plan.items : (long long)a.tok.n_tokens * a.Hkv;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  void* args[] = {&wa};
+  return launch_pdl(fn, dim3((unsigned)blocks), dim3(32 * Ring<INT4>::kWarps), smem, stream, args);
 }
 
 }  // namespace
 
-// Items per (query, KV head): the fewest waves of blocks (one per SM) times a block's length, which is a
-// fixed part (the queries, the first copies, the join: about kFixed units of a warp's time) and the units
-// per warp.  At most four blocks per SM are split off, so the workspace has one size for every call.
+// Blocks of a call: what the GPU holds at once, but no more than give a warp two units.  Many rows are not cut
+// (items 0): a block takes a whole pair.
 WindowPlan plan_window(bool int4, int64_t rows, int Hq, int Hkv, int64_t max_keys, int num_sms) {
   WindowPlan p;
-  const int warps = int4 ? Ring<true>::kWarps : Ring<false>::kWarps;
+  const int warps = int4 ? Ring<true>::kWarps : Ring<false>::kWarps, per_sm = int4 ? Ring<true>::kBlocks : Ring<false>::kBlocks;
   const int tok = 16 * (int4 ? Ring<true>::kTiles : Ring<false>::kTiles);
-  const int64_t units = (max_keys + 2 * tok - 2) / tok + 1, pairs = std::max<int64_t>(rows * Hkv, 1);
-  constexpr int kFixed = 10;
-  const int64_t most = std::min<int64_t>((units + warps - 1) / warps, kSplitBlocks * (int64_t)num_sms / pairs);
-  int64_t best = INT64_MAX;
-  for (int64_t n = 1; n <= std::max<int64_t>(most, 1); ++n) {
-    const int64_t waves = (pairs * n + num_sms - 1) / std::max(num_sms, 1);
-    const int64_t cost = waves * (kFixed + (units + n * warps - 1) / (n * warps) + (n > 1 ? 2 : 0));
-    if (cost < best) {
-      best = cost;
-      p.items = (int)n;
-    }
-  }
-  p.off_records = ((size_t)kSplitBlocks * num_sms * sizeof(unsigned) + 255) & ~(size_t)255;
-  p.total = p.off_records + (size_t)kSplitBlocks * num_sms * (Hq / Hkv) * (kD + 2) * sizeof(float);
+  const int64_t units = rows * Hkv * ((max_keys + tok - 1) / tok + 1);
+  if (rows <= kMaxRows && units < (INT64_C(1) << 30))
+    p.items = (int)std::min<int64_t>((int64_t)per_sm * num_sms, std::max<int64_t>(1, units / (2 * warps)));
+  else
+    p.items = 0;
+  const int64_t most = (int64_t)std::max(Ring<true>::kBlocks, Ring<false>::kBlocks) * num_sms;
+  p.off_records = ((size_t)most * sizeof(unsigned) + 255) & ~(size_t)255;
+  p.total = p.off_records + (size_t)most * 2 * ((Hq / Hkv) * (kD + 2) + 3) * sizeof(float);
   return p;
 }
 
