@@ -31,15 +31,20 @@ namespace {
 constexpr float kLog2eW = 1.4426950408889634f;
 constexpr float kLazyW = 8.0f;  // the accumulators are rescaled when the maximum grows by more than 2^8
 
-template <bool INT4>
+// WIDE: 16 warps and one block per SM (4 bits), for few pairs, whose cuts each cost a join (batch 1 x 100K, 8
+// pairs: 29.9 us, 33.3 us with two blocks of 8); else two blocks of 8, one of which copies and computes while the
+// other begins or joins a segment (28 requests x 4160 visible keys, 224 pairs: 39.4 us against 44.3; 8 ragged
+// requests, 64 pairs: 138 against 142).  BF16 has one block of 8 (its units are larger).
+template <bool INT4, bool WIDE>
 struct Ring {
-  static constexpr int kWarps = INT4 ? 16 : 8;
-  static constexpr int kBlocks = 1;                       // blocks per SM
+  static constexpr int kWarps = INT4 && WIDE ? 16 : 8;
+  static constexpr int kBlocks = INT4 && !WIDE ? 2 : 1;              // blocks per SM
   static constexpr int kTiles = INT4 ? 2 : 1;                        // 16-token tiles of a unit
   static constexpr int kUnit = INT4 ? 2 * kTile4Bytes : 16 * kD * 4;  // bytes of a unit
   static constexpr int kStages = 3;
   static constexpr int kBytes = kWarps * kStages * kUnit;
 };
+constexpr int kWidePairs = 32;  // (query, KV head) pairs from which on the blocks are the smaller ones
 constexpr int kSlack = 8;
 constexpr int kMaxRows = 1024;  // query rows whose lengths a block adds up; with more, a block takes one whole pair
 
@@ -224,9 +229,9 @@ __device__ __forceinline__ uint32_t split_bf16(float x) {
   return pack_bf16x2(v, x - v);
 }
 
-template <bool PACK, bool INT4>
+template <bool PACK, bool INT4, bool WIDE>
 __device__ __forceinline__ void window_body(const WindowArgs& wa) {
-  using R = Ring<INT4>;
+  using R = Ring<INT4, WIDE>;
   constexpr int kW = R::kWarps, kS = R::kStages, KU = R::kTiles, kH = PACK ? 1 : 2;
   const WindowLaunch& a = wa.a;
   extern __shared__ __align__(128) uint8_t sm[];
@@ -798,18 +803,19 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   }
 }
 
-template <bool PACK, bool INT4>
-__global__ void __launch_bounds__(32 * Ring<INT4>::kWarps, Ring<INT4>::kBlocks) window_split_kernel(const __grid_constant__ WindowArgs wa) {
-  window_body<PACK, INT4>(wa);
+template <bool PACK, bool INT4, bool WIDE>
+__global__ void __launch_bounds__(32 * Ring<INT4, WIDE>::kWarps, Ring<INT4, WIDE>::kBlocks)
+    window_split_kernel(const __grid_constant__ WindowArgs wa) {
+  window_body<PACK, INT4, WIDE>(wa);
 }
 
-template <bool PACK, bool INT4>
+template <bool PACK, bool INT4, bool WIDE>
 cudaError_t launch_one(const WindowLaunch& a, cudaStream_t stream) {
+  using R = Ring<INT4, WIDE>;
   static std::atomic<uint64_t> done;
-  const void* fn = reinterpret_cast<const void*>(window_split_kernel<PACK, INT4>);
-  constexpr size_t smem = Ring<INT4>::kBytes;
-  static_assert(Ring<INT4>::kWarps * kMaxG * kD * 4 <= Ring<INT4>::kBytes, "the warps' accumulators in the ring");
-  const cudaError_t e = smem_attr_once(fn, smem, done);
+  const void* fn = reinterpret_cast<const void*>(window_split_kernel<PACK, INT4, WIDE>);
+  static_assert(R::kWarps * kMaxG * kD * 4 <= R::kBytes, "the warps' accumulators in the ring");
+  const cudaError_t e = smem_attr_once(fn, R::kBytes, done);
   if (e != cudaSuccess) return e;
   WindowArgs wa;
   wa.a = a;
@@ -817,7 +823,15 @@ cudaError_t launch_one(const WindowLaunch& a, cudaStream_t stream) {
   const long long blocks = wa.cut ? a.plan.items : (long long)a.tok.n_tokens * a.Hkv;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   void* args[] = {&wa};
-  return launch_pdl(fn, dim3((unsigned)blocks), dim3(32 * Ring<INT4>::kWarps), smem, stream, args);
+  return launch_pdl(fn, dim3((unsigned)blocks), dim3(32 * R::kWarps), R::kBytes, stream, args);
+}
+
+bool wide(int64_t rows, int Hkv) { return rows * Hkv < kWidePairs; }
+
+template <bool INT4, bool WIDE>
+int blocks_of(int64_t units, int num_sms) {
+  using R = Ring<INT4, WIDE>;
+  return (int)std::min<int64_t>((int64_t)R::kBlocks * num_sms, std::max<int64_t>(1, units / (2 * R::kWarps)));
 }
 
 }  // namespace
@@ -826,14 +840,13 @@ cudaError_t launch_one(const WindowLaunch& a, cudaStream_t stream) {
 // (items 0): a block takes a whole pair.
 WindowPlan plan_window(bool int4, int64_t rows, int Hq, int Hkv, int64_t max_keys, int num_sms) {
   WindowPlan p;
-  const int warps = int4 ? Ring<true>::kWarps : Ring<false>::kWarps, per_sm = int4 ? Ring<true>::kBlocks : Ring<false>::kBlocks;
-  const int tok = 16 * (int4 ? Ring<true>::kTiles : Ring<false>::kTiles);
+  const int tok = 16 * (int4 ? Ring<true, true>::kTiles : Ring<false, true>::kTiles);
   const int64_t units = rows * Hkv * ((max_keys + tok - 1) / tok + 1);
-  if (rows <= kMaxRows && units < (INT64_C(1) << 30))
-    p.items = (int)std::min<int64_t>((int64_t)per_sm * num_sms, std::max<int64_t>(1, units / (2 * warps)));
-  else
-    p.items = 0;
-  const int64_t most = (int64_t)std::max(Ring<true>::kBlocks, Ring<false>::kBlocks) * num_sms;
+  p.items = rows > kMaxRows || units >= (INT64_C(1) << 30) ? 0
+            : !int4               ? blocks_of<false, true>(units, num_sms)
+            : wide(rows, Hkv)     ? blocks_of<true, true>(units, num_sms)
+                                  : blocks_of<true, false>(units, num_sms);
+  const int64_t most = (int64_t)Ring<true, false>::kBlocks * num_sms;  // blocks of any call
   p.off_records = ((size_t)most * sizeof(unsigned) + 255) & ~(size_t)255;
   p.total = p.off_records + (size_t)most * 2 * ((Hq / Hkv) * (kD + 2) + 3) * sizeof(float);
   return p;
@@ -841,8 +854,10 @@ WindowPlan plan_window(bool int4, int64_t rows, int Hq, int Hkv, int64_t max_key
 
 cudaError_t launch_window_split(const WindowLaunch& a, cudaStream_t stream) {
   const bool pack = a.Hq / a.Hkv <= 4;
-  if (a.pages4 != nullptr) return pack ? launch_one<true, true>(a, stream) : launch_one<false, true>(a, stream);
-  return pack ? launch_one<true, false>(a, stream) : launch_one<false, false>(a, stream);
+  if (a.pages4 == nullptr) return pack ? launch_one<true, false, true>(a, stream) : launch_one<false, false, true>(a, stream);
+  if (wide(a.tok.n_tokens, a.Hkv))
+    return pack ? launch_one<true, true, true>(a, stream) : launch_one<false, true, true>(a, stream);
+  return pack ? launch_one<true, true, false>(a, stream) : launch_one<false, true, false>(a, stream);
 }
 
 }  // namespace oscar
