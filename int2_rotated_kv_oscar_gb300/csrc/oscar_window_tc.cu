@@ -8,18 +8,23 @@
 //   S = Q K^T   M 128 (rows), N 128 (keys), K 16 a step; both from shared memory
 //   P = exp2(c S - m), rounded to bf16 (one term, at most 2^-8 of a weight, as
 //       the result is; c = sm_scale log2 e, m the row's running maximum)
-//   O += P V    P from tensor memory (over half of S's columns), V as it lies in
+//   O += P V    P from tensor memory (over S's columns), V as it lies in
 //       the page: keys along K, channels contiguous (an "MN-major" operand)
 // with S, O and the sums in fp32.  Tensor memory: S of both tiles (2 x 128
 // columns), O of both (2 x 128).
 //
-//   warps 0-3, 4-7  softmax of tile 0, 1: a thread is a row (its TMEM lane)
-//   warp 8          copies K and V blocks (TMA, 64 channels x 64 rows, 128-byte
-//                   swizzle) into a ring of five 32 KB slots, in the order of
-//                   use: K_0, V_0, K_1, V_1, ...
-//   warp 9          one thread issues the MMAs: S_t(j + 1) right behind
-//                   P_t V(j), so that one tile's softmax runs under the other
-//                   tile's products
+//   warps 0-15   softmax: tile w / 8, keys 64 (w / 4 % 2) .. + 63 of a block; a
+//                thread is half a row (its TMEM lane), so that the time from S to
+//                P, which the products wait for, is that of 64 exponentials
+//   warp 16      copies K and V blocks (TMA, 64 channels x 64 rows, 128-byte
+//                swizzle) into a ring of five 32 KB slots, in the order of
+//                use: K_0, V_0, K_1, V_1, ...
+//   warp 17      one thread issues the MMAs, tile by tile: S_t(j + 1) right
+//                behind P_t V(j), so that one tile's softmax runs under the other
+//                tile's products
+//   warps 18, 19 wait for the products of tile 0, 1 and meet its softmax warps at
+//                a hardware barrier: sixteen warps that poll took more issue slots
+//                than their exponentials
 // A block sees only the pages that some of its queries see.  With few blocks
 // the keys are split over several (items) whose records (m, l, O) the last one
 // to finish joins in item order.
@@ -37,14 +42,20 @@ namespace oscar {
 namespace {
 
 constexpr float kLog2eT = 1.4426950408889634f;
-constexpr int kTcwThreads = 10 * 32;
+constexpr int kTcwThreads = 20 * 32;
+constexpr int kTcwCopy = 16, kTcwMma = 17, kTcwRelay = 18;  // warps
 constexpr int kTcwSlots = 5;
 constexpr uint32_t kTcwQ = 0;                    // queries: [tile][2 x 64 channels][128 rows][128 B]
 constexpr uint32_t kTcwRing = 65536;             // slots: [2 x 64 channels][128 keys][128 B]
 constexpr uint32_t kTcwBars = kTcwRing + kTcwSlots * 32768;
-constexpr size_t kTcwSmem = kTcwBars + 256 + 1024;  // + 1024-byte alignment slack
+constexpr uint32_t kTcwX = kTcwBars + 256;        // what the two halves of a row tell each other: [tile][half][128 rows] float
+constexpr size_t kTcwSmem = kTcwX + 2048;        // (all of it dynamic, so that it begins where the block's memory does)
 constexpr uint32_t kTmS = 0, kTmO = 256;         // TMEM columns of S and O, 128 a tile
-constexpr float kLazyT = 8.0f;                   // O moves when a row's maximum grew by more than 2^8
+// A row's weights are taken relative to the maximum of the first block that it saw something of, until half a
+// block's sum of them reaches kTopSum (2^40; fp32 and bf16 reach 2^127): then the maximum is found anew, and O
+// and l move.  So the common block needs no maximum: its exponentials start with the first logits that arrive
+// (a block that moves takes 2000 cycles more; at 2^16 every fifth block did).
+constexpr float kTopSum = 1099511627776.0f;
 constexpr int kRowFloats = kD + 2;               // a row's record: O[128], m, l
 
 struct TcwArgs {
@@ -73,29 +84,70 @@ __device__ __forceinline__ float exp2_t(float x) {
   return y;
 }
 
-// Logits of positions at, at + 1, ... that the row does not see drop out.
-__device__ __forceinline__ void hide(float (&s)[32], int at, int lim, int sinks, int low) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (!(at + e < lim && (at + e < sinks || at + e >= low))) s[e] = -INFINITY;
+// 32 columns of this thread's lane, in flight until the wait that names the same registers.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
-__device__ __forceinline__ float max32(const float (&s)[32]) {
-  float m[4] = {s[0], s[1], s[2], s[3]};
+// The n lowest of 32 bits (n may lie outside 0..32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Logits whose bit in `seen` is 0 drop out.
+__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t seen) {
 #pragma unroll
-  for (int e = 4; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], s[e]);
+  for (int e = 0; e < 32; ++e)
+    if (!(seen & (1u << e))) s[e] = 0xff800000u;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float m[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
+#pragma unroll
+  for (int e = 4; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(s[e]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 // exp2(c s - mc) of 32 logits: their sum, and 16 pairs of bf16.
-__device__ __forceinline__ void weights(const float (&s)[32], float c, float mc, float2& sum, uint32_t* w) {
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], float c, float mc, float2& sum, uint32_t* w) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    const float2 y = ffma2(make_float2(s[e], s[e + 1]), make_float2(c, c), make_float2(-mc, -mc));
+    const float2 y = ffma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(c, c),
+                           make_float2(-mc, -mc));
     const float2 p = make_float2(exp2_t(y.x), exp2_t(y.y));
     sum = fadd2(sum, p);
     w[e >> 1] = pack_bf16x2(p.x, p.y);
   }
+}
+
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+  return x != 0;
+}
+
+// Whether any thread of the two warps at named barrier `id` says so in round `round` (> 0, and larger each time):
+// a word of shared memory that only a thread with news writes.
+__device__ __forceinline__ bool pair_any(int id, volatile int* word, int round, bool x) {
+  if (x) *word = round;
+  group_sync(id, 64);
+  return *word == round;
 }
 
 // The pages that some query of a block sees: logical pages [0, sp) and [wb, we).
@@ -109,9 +161,9 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     window_tc_kernel(const __grid_constant__ TcwArgs ta, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv) {
   const WindowLaunch& a = ta.a;
-  extern __shared__ uint8_t raw[];
-  __shared__ int sm_last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  // (by way of a shuffle, so that the compiler knows the warp's role to be uniform)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // block -> (tile pair, request, KV head, item); later tiles (more keys) first
   int x = blockIdx.x;
   const int item = x % ta.items;
@@ -153,15 +205,18 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
   for (int k = 2 * j0 + threadIdx.x; k < min(2 * j1, np); k += kTcwThreads)
     bad = bad || page_of(a.pages, b, pl.page(k), a.err, true) < 0;
 
-  const uint32_t raw_s = smem_u32(raw);
-  uint8_t* sm = raw + (((raw_s + 1023u) & ~1023u) - raw_s);
   const uint32_t sbase = smem_u32(sm);
+  float(*sm_x)[2][128] = reinterpret_cast<float(*)[2][128]>(sm + kTcwX);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + kTcwBars);  // [slots] copies landed
   uint64_t* empty = full + kTcwSlots;                           // [slots] read by its products
   uint64_t* sfull = empty + kTcwSlots;                          // [2] S of tile t holds a block's logits (and O its last product)
   uint64_t* pready = sfull + 2;                                 // [2] P of tile t written
   uint64_t* odone = pready + 2;                                 // [2] O of tile t complete
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(odone + 2);
+  volatile int* last = reinterpret_cast<volatile int*>(tmem_at + 1);
+  volatile int* dead = last + 1;  // [2] a relay's wait gave up
+  if (threadIdx.x < 8) reinterpret_cast<int*>(sm + kTcwBars + 192)[threadIdx.x] = 0;  // the pairs' words
+  if (threadIdx.x < 2) dead[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTcwSlots; ++i) {
       mbar_init(&full[i], 1);
@@ -169,37 +224,37 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pready[t], 4);
+      mbar_init(&pready[t], 8);
       mbar_init(&odone[t], 1);
     }
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(tmem_at, 512);
-  if (warp == 8 && lane == 0) {
+  if (warp == kTcwMma) tmem_alloc(tmem_at, 512);
+  if (warp == kTcwCopy && lane == 0) {
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
   }
-  const int t = warp >> 2, row = 32 * (warp & 3) + lane;  // softmax warps: tile and row
+  const int t = warp >> 3, hf = (warp >> 2) & 1, row = 32 * (warp & 3) + lane;  // softmax warps: tile, half and row
   const int qi = i0 + t * qpt + row / g, head = row % g;
-  const bool live = warp < 8 && row < qpt * g && qi < n;
-  if (warp < 8 && t < ntile) {  // the queries, into the swizzled operand layout
+  const bool live = warp < kTcwCopy && row < qpt * g && qi < n;
+  if (warp < kTcwCopy && t < ntile) {  // the queries, into the swizzled operand layout
     const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(row0 + qi) * a.q_stride + (size_t)(h * g + head) * kD);
     uint8_t* dst = sm + kTcwQ + t * 32768 + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const uint4 v = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = v;
+    for (int c = 0; c < 8; ++c) {
+      const uint4 v = live ? src[8 * hf + c] : make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(dst + hf * 16384 + ((c ^ (row & 7)) << 4)) = v;
     }
     fence_proxy_async_smem();
   }
   tc_fence_before();
   const bool any_bad = __syncthreads_or(bad);
   tc_fence_after();
-  const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(tmem_at);
+  const uint32_t tbase = 0;  // (an allocation of all 512 columns begins at column 0)
   bool gave_up = false;
 
   float m = -INFINITY, l = 0.f;
-  if (warp == 8) {
+  if (warp == kTcwCopy) {
     // ---- copies: use 0 is K_0, 2 j + 1 is V_j, 2 j + 2 is K_(j + 1)
     int phys_l = -1, fetched = 0;
     auto phys_of = [&](int k) {  // k-th page of this item (whole warp)
@@ -251,9 +306,21 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
         mbar_wait_timed(&full[i], 1, kWaitNs);
       }
     }
-  } else if (warp == 9) {
-    // ---- products, issued by one thread
-    if (lane == 0 && nb > 0) {
+  } else if (warp >= kTcwRelay) {
+    // ---- relays
+    const int tt = warp - kTcwRelay;
+    for (int j = 0; j <= nb && tt < ntile && nb > 0; ++j) {
+      if (!gave_up) gave_up = !__all_sync(0xffffffffu, j < nb ? mbar_wait_timed(&sfull[tt], j & 1, kWaitNs)
+                                                              : mbar_wait_timed(&odone[tt], 0, kWaitNs));
+      if (gave_up && lane == 0) dead[tt] = 1;
+      group_sync(9 + tt, 288);
+    }
+    if (gave_up && lane == 0) set_error(a.err, kErrTimeout);
+  } else if (warp > kTcwCopy) {
+    // ---- products, issued by one thread, the tiles in turn: that keeps one tile's softmax under the other's
+    // products (with a thread for each tile the two fall into step: 4650 cycles a pair of blocks)
+    const int nb = __shfl_sync(0xffffffffu, j1 - j0, 0), nt = __shfl_sync(0xffffffffu, ntile, 0);  // uniform
+    if (nb > 0) {
       constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, 128);
       constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, 128) | (1u << 16);  // B: channels contiguous
       auto logits = [&](int tt, int slot) {
@@ -261,159 +328,186 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-          umma_f16(tbase + kTmS + tt * 128, umma_desc_sw128(q + off), umma_desc_sw128(k + off), idesc_s, s > 0);
+          umma_f16(kTmS + tt * 128, umma_desc_sw128(q + off), umma_desc_sw128(k + off), idesc_s, s > 0);
         }
         umma_commit(&sfull[tt]);
       };
-      bool ok = mbar_wait_timed(&full[0], 0, kWaitNs);
+      // (the whole warp waits and loops, so that addresses stay in uniform registers; one elected thread issues)
+      auto landed = [&](int u) {
+        return __all_sync(0xffffffffu, mbar_wait_timed(&full[u % kTcwSlots], (u / kTcwSlots) & 1, kWaitNs)) != 0;
+      };
+      bool ok = landed(0);
       if (ok) {
         tc_fence_after();
-        for (int tt = 0; tt < ntile; ++tt) logits(tt, 0);
-        umma_commit(&empty[0]);
+        if (elect_one()) {
+          for (int tt = 0; tt < nt; ++tt) logits(tt, 0);
+          umma_commit(&empty[0]);
+        }
+        __syncwarp();
+        ok = landed(1);
       }
+      // Between a tile's products and the next one's there is nothing but the wait for P: the slots' releases and
+      // the waits for copies come behind products that are still running.
       for (int j = 0; j < nb && ok; ++j) {
-        const int uv = 2 * j + 1, uk = 2 * j + 2, sv = uv % kTcwSlots, sk = uk % kTcwSlots;
-        ok = mbar_wait_timed(&full[sv], (uv / kTcwSlots) & 1, kWaitNs);
-        for (int tt = 0; tt < ntile && ok; ++tt) {
-          ok = mbar_wait_timed(&pready[tt], j & 1, kWaitNs);
+        const int sv = (2 * j + 1) % kTcwSlots, sk = (2 * j + 2) % kTcwSlots, before = (2 * j) % kTcwSlots;
+        const bool more = j + 1 < nb;
+        for (int tt = 0; tt < nt; ++tt) {
+          ok = __all_sync(0xffffffffu, mbar_wait_timed(&pready[tt], j & 1, kWaitNs));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v = sbase + kTcwRing + sv * 32768;
+          if (elect_one()) {
+            const uint32_t v = sbase + kTcwRing + sv * 32768, tS = kTmS + tt * 128;
 #pragma unroll
-          for (int s = 0; s < 8; ++s)
-            umma_f16_ts(tbase + kTmO + tt * 128, tbase + kTmS + tt * 128 + 64 + 8 * s, umma_desc_mn_sw128(v + 2048 * s, 16384, 1024),
-                        idesc_o, j > 0 || s > 0);
-          if (j + 1 < nb) {
-            if (tt == 0) ok = mbar_wait_timed(&full[sk], (uk / kTcwSlots) & 1, kWaitNs);
-            if (ok) {
-              tc_fence_after();
-              logits(tt, sk);
-            }
-          } else {
-            umma_commit(&odone[tt]);
+            for (int s = 0; s < 8; ++s)  // P: keys 0-63 in S's columns 0-31, the others in 64-95
+              umma_f16_ts(kTmO + tt * 128, tS + (s >> 2) * 64 + 8 * (s & 3), umma_desc_mn_sw128(v + 2048 * s, 16384, 1024),
+                          idesc_o, j > 0 || s > 0);
+            if (!more) umma_commit(&odone[tt]);
+            if (more && tt == 0 && j > 0) umma_commit(&empty[before]);  // K_j, whose last product is behind the last V's
+            if (more && tt == nt - 1) umma_commit(&empty[sv]);
+          }
+          __syncwarp();
+          if (!more) continue;
+          if (tt == 0) {
+            ok = landed(2 * j + 2);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (elect_one()) logits(tt, sk);
+          __syncwarp();
+          if (tt == 0) {
+            ok = landed(2 * j + 3);
+            if (!ok) break;
           }
         }
-        if (ok) {
-          umma_commit(&empty[sv]);
-          if (j + 1 < nb) umma_commit(&empty[sk]);
-        }
       }
-      if (!ok) set_error(a.err, kErrTimeout);
+      if (!ok && lane == 0) set_error(a.err, kErrTimeout);
     }
     __syncwarp();
   } else if (t < ntile) {
-    // ---- softmax: this thread's row
-    const uint32_t ts = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + kTmS + t * 128;
-    const uint32_t to = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + kTmO + t * 128;
+    // ---- softmax: this thread's half of a row
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tbase + lanes + kTmS + t * 128 + hf * 64, to = tbase + lanes + kTmO + t * 128 + hf * 64;
+    const int pair_bar = 1 + 4 * t + (warp & 3);  // named barrier of the two warps that share these rows
+    volatile int* pair_word = reinterpret_cast<volatile int*>(sm + kTcwBars + 192) + 4 * t + (warp & 3);
     const float c = a.sm_scale * kLog2eT;
     const int tf = first + t * qpt, tl = min(tf + qpt - 1, (int)plast);  // the tile's positions
     const int p = min(p0 + qi, (int)plast);
     const int lim = min(p + 1, ctx), low = a.window < 0 ? 0 : max(0, p - a.window + 1);
+    // pages (of the block's list) of which every row of the tile sees all: [k_lo, k_hi), past the sinks
+    const int k_lo = pl.sp + max(0, (a.window < 0 ? 0 : max(0, tl - a.window + 1) + kPage - 1) / kPage - pl.wb);
+    const int k_hi = any_bad ? 0 : pl.sp + min(tf + 1, ctx) / kPage - pl.wb;
     for (int j = 0; j < nb; ++j) {
-      // the block's pages: whether every row of the tile sees all of them, and whether some row of theirs is
-      // seen by no query of the block (such a V row may hold anything: it becomes zeros)
-      int base[2];
-      bool whole = true, clean = true;
+      const int k0 = 2 * (j0 + j);
+      const bool whole = k0 >= k_lo && k0 + 1 < k_hi;
+      uint32_t seen[2] = {~0u, ~0u};  // the row's keys of this half
+      if (!whole) {
+        // (a page outside the pool, or none: past every position)
+        int base[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int kk = 2 * (j0 + j) + k;
-        const int lp = kk < np ? pl.page(kk) : -1;
-        base[k] = lp < 0 || (any_bad && page_of(a.pages, b, lp, a.err, false) < 0) ? INT32_MAX - 63 : lp * kPage;
-        const int end = base[k] + 63;
-        whole = whole && end < min(tf + 1, ctx) && (end < sinks || a.window < 0 || base[k] > tl - a.window);
-        clean = clean && end < hi && (end < sinks || base[k] >= lo);
-      }
-      if (t == 0 && !clean) {
-        const int uv = 2 * j + 1, sv = uv % kTcwSlots;
-        if (!__all_sync(0xffffffffu, mbar_wait_timed(&full[sv], (uv / kTcwSlots) & 1, kWaitNs))) {
-          gave_up = true;
-          break;
+        for (int k = 0; k < 2; ++k) {
+          const int lp = k0 + k < np ? pl.page(k0 + k) : -1;
+          base[k] = lp < 0 || (any_bad && page_of(a.pages, b, lp, a.err, false) < 0) ? INT32_MAX - 63 : lp * kPage;
         }
+        // a V row that no query of the block sees may hold anything: it becomes zeros (by both tiles, each before
+        // its own product)
         const int at = (row < 64 ? base[0] : base[1]) + (row & 63);
-        if (!(at < hi && (at < sinks || at >= lo))) {
-          uint8_t* v = sm + kTcwRing + sv * 32768 + row * 128;
+        const bool stale = !(at < hi && (at < sinks || at >= lo));
+        if (__any_sync(0xffffffffu, stale) && !gave_up) {
+          const int uv = 2 * j + 1, sv = uv % kTcwSlots;
+          gave_up = !__all_sync(0xffffffffu, mbar_wait_timed(&full[sv], (uv / kTcwSlots) & 1, kWaitNs));
+          if (!gave_up && stale) {
+            uint8_t* v = sm + kTcwRing + sv * 32768 + hf * 16384 + row * 128;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            *reinterpret_cast<uint4*>(v + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(v + 16384 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(v + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
           }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int p32 = base[hf] + 32 * k;
+          seen[k] = low_bits(lim - p32) & (low_bits(sinks - p32) | ~low_bits(low - p32));
+        }
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_timed(&sfull[t], j & 1, kWaitNs))) {
-        gave_up = true;
-        break;
-      }
+      // after a wait that gave up, the loop goes on without tensor memory: the barriers still meet
+      group_sync(9 + t, 288);
+      gave_up = gave_up || dead[t] != 0;
       tc_fence_after();
-      // the first 64 keys are read twice (once for the maximum), the others stay in registers; P goes over the
-      // others' columns
-      float s0[32], s1[32], s2[32], s3[32];
-      tmem_ld32x2(ts, ts + 32, s0, s1);
-      if (!whole) {
-        hide(s0, base[0], lim, sinks, low);
-        hide(s1, base[0] + 32, lim, sinks, low);
+      uint32_t w[32];
+      float2 sum = make_float2(0.f, 0.f);
+      float mc = m == -INFINITY ? 0.f : m * c;
+      if (!gave_up) {
+        uint32_t s0[32], s1[32];
+        tmem_ld32_start(ts, s0);
+        tmem_ld32_wait(s0);
+        tmem_ld32_start(ts + 32, s1);
+        if (!whole) hide(s0, seen[0]);
+        weights(s0, c, mc, sum, w);
+        tmem_ld32_wait(s1);
+        if (!whole) hide(s1, seen[1]);
+        weights(s1, c, mc, sum, w + 16);
       }
-      const float ma = fmaxf(max32(s0), max32(s1));
-      tmem_ld32x2(ts + 64, ts + 96, s2, s3);
-      if (!whole) {
-        hide(s2, base[1], lim, sinks, low);
-        hide(s3, base[1] + 32, lim, sinks, low);
-      }
-      const float mb = fmaxf(ma, fmaxf(max32(s2), max32(s3)));
-      // m, in units of S; O and l move when it grew by more than 2^8 in the exponent
-      const bool grow = (mb - m) * c > kLazyT || (m == -INFINITY && mb > -INFINITY);
-      if (__any_sync(0xffffffffu, grow)) {
+      const bool move = !(sum.x + sum.y < kTopSum) || (m == -INFINITY && (seen[0] | seen[1]) != 0);
+      if (pair_any(pair_bar, pair_word, j + 1, move)) {
+        // the logits are still in place: the rows' maxima anew, O and l along, and the weights again
+        uint32_t s0[32];
+        float mb = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < 2 && !gave_up; ++k) {
+          tmem_ld32_start(ts + 32 * k, s0);
+          tmem_ld32_wait(s0);
+          hide(s0, k ? seen[1] : seen[0]);
+          mb = fmaxf(mb, max32(s0));
+        }
+        sm_x[t][hf][row] = mb;
+        group_sync(pair_bar, 64);
+        mb = fmaxf(mb, sm_x[t][hf ^ 1][row]);
         float f = 1.f;
-        if (grow) {
+        // (a half's sum of kTopSum holds a weight of 2^10 at least, so the row that asked for it does move)
+        if (mb > m && (m == -INFINITY || (mb - m) * c > 8.f)) {
           f = m == -INFINITY ? 0.f : exp2_t((m - mb) * c);
           m = mb;
           l *= f;
         }
-        if (j > 0) {
+        mc = m == -INFINITY ? 0.f : m * c;
+        sum = make_float2(0.f, 0.f);
+        if (!gave_up) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float o[32];
-            tmem_ld32(to + 32 * k, o);
+          for (int k = 0; k < 2; ++k) {
+            if (j > 0) {
+              float o[32];
+              tmem_ld32(to + 32 * k, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tmem_st32(to + 32 * k, o);
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(to + 32 * k, o);
+            }
+            tmem_ld32_start(ts + 32 * k, s0);
+            tmem_ld32_wait(s0);
+            hide(s0, seen[k]);
+            weights(s0, c, mc, sum, w + 16 * k);
           }
         }
       }
-      const float mc = m == -INFINITY ? 0.f : m * c;
-      float2 sum = make_float2(0.f, 0.f);
-      uint32_t w[32];
-      weights(s2, c, mc, sum, w);
-      weights(s3, c, mc, sum, w + 16);
-      tmem_st32u(ts + 96, w);
-      tmem_ld32x2(ts, ts + 32, s0, s1);
-      if (!whole) {
-        hide(s0, base[0], lim, sinks, low);
-        hide(s1, base[0] + 32, lim, sinks, low);
-      }
-      weights(s0, c, mc, sum, w);
-      weights(s1, c, mc, sum, w + 16);
-      tmem_st32u(ts + 64, w);
       l += sum.x + sum.y;
-      tmem_wait_st();
+      if (!gave_up) {
+        tmem_st32u(ts, w);
+        tmem_wait_st();
+      }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pready[t]);
+      if (lane == 0 && !gave_up) mbar_arrive(&pready[t]);
     }
-    if (gave_up && lane == 0) set_error(a.err, kErrTimeout);
-    if (!gave_up && nb > 0) {
-      if (!__all_sync(0xffffffffu, mbar_wait_timed(&odone[t], 0, kWaitNs))) {
-        gave_up = true;
-        if (lane == 0) set_error(a.err, kErrTimeout);
-      }
-      tc_fence_after();
-    }
+    if (nb > 0) group_sync(9 + t, 288);  // O is complete (and the row's last exchange is read)
+    gave_up = gave_up || dead[t] != 0;
+    tc_fence_after();
+    sm_x[t][hf][row] = l;
+    group_sync(pair_bar, 64);
+    l += sm_x[t][hf ^ 1][row];
     const bool got = !gave_up && nb > 0;
     if (ta.items == 1) {
       const float f = l > 0.f ? 1.f / l : 0.f;
-      uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)(row0 + qi) * a.Hq + h * g + head) * kD);
+      uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)(row0 + qi) * a.Hq + h * g + head) * kD + 64 * hf);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 2; ++k) {
         float o[32];
         if (got) tmem_ld32(to + 32 * k, o);
         if (live)
@@ -431,25 +525,25 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
       float* rec = reinterpret_cast<float*>(a.workspace + a.plan.off_records) +
                    ((size_t)blockIdx.x * 256 + 128 * t + row) * kRowFloats;
       if (!got) m = -INFINITY;
-      if (live) {
+      if (live && hf == 0) {
         rec[kD] = m;
         rec[kD + 1] = l;
       }
       if (got)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
           float o[32];
           tmem_ld32(to + 32 * k, o);
           if (live)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2*>(rec + 32 * k + e) = make_float2(o[e], o[e + 1]);
+            for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2*>(rec + 64 * hf + 32 * k + e) = make_float2(o[e], o[e + 1]);
         }
     }
   }
   tc_fence_before();
   if (ta.items > 1) __threadfence();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kTcwMma) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
@@ -458,11 +552,11 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
   const unsigned group = blockIdx.x / ta.items;
   if (threadIdx.x == 0) {
     unsigned* counter = reinterpret_cast<unsigned*>(a.workspace) + group;
-    sm_last = atomicAdd(counter, 1u) == (unsigned)ta.items - 1u;
-    if (sm_last) *counter = 0u;
+    *last = atomicAdd(counter, 1u) == (unsigned)ta.items - 1u;
+    if (*last) *counter = 0u;
   }
   __syncthreads();
-  if (!sm_last) return;
+  if (!*last) return;
   __threadfence();
   const float c = a.sm_scale * kLog2eT;
   const float* recs = reinterpret_cast<const float*>(a.workspace + a.plan.off_records) + (size_t)group * ta.items * 256 * kRowFloats;
