@@ -63,11 +63,23 @@ struct TcwArgs {
   int items, tiles, qpt;  // blocks per (tile pair, KV head), tile pairs per request, queries per tile
 };
 
-// Operand with its M or N index contiguous, 128-byte swizzle: rows (K) of 64 elements (128 bytes), groups of
-// 8 rows `sbo` bytes apart, the next 64 elements `lbo` bytes on.
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// D[tmem] (+)= A[smem] B[smem]^T and A[tmem] B[smem], the operands' descriptors as their low words (start address
+// / 16, and above it the leading offset / 16) with one high word.  A K-major operand in the 128-byte swizzle has
+// rows of 64 elements and groups of 8 rows 1024 bytes apart (the leading offset is not used); an operand with its
+// N index contiguous has K as the rows, and the next 64 of N a leading offset on.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_load_page(void* dst, const void* tmap, int c0, int c1, int c2, uint64_t* bar) {
@@ -224,7 +236,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sfull[t], 1);
-      mbar_init(&pready[t], 8);
+      mbar_init(&pready[t], 9);  // the tile's softmax warps, and its relay for the copies
       mbar_init(&odone[t], 1);
     }
     fence_mbar_init();
@@ -307,36 +319,42 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
       }
     }
   } else if (warp >= kTcwRelay) {
-    // ---- relays
+    // ---- relays: the products' logits to the softmax warps, and the copies that the next products read
     const int tt = warp - kTcwRelay;
+    auto landed = [&](int u) {
+      return __all_sync(0xffffffffu, mbar_wait_timed(&full[u % kTcwSlots], (u / kTcwSlots) & 1, kWaitNs)) != 0;
+    };
     for (int j = 0; j <= nb && tt < ntile && nb > 0; ++j) {
       if (!gave_up) gave_up = !__all_sync(0xffffffffu, j < nb ? mbar_wait_timed(&sfull[tt], j & 1, kWaitNs)
                                                               : mbar_wait_timed(&odone[tt], 0, kWaitNs));
       if (gave_up && lane == 0) dead[tt] = 1;
       group_sync(9 + tt, 288);
+      if (j < nb && !gave_up) {
+        gave_up = !landed(2 * j + 1) || (j + 1 < nb && !landed(2 * j + 2));
+        if (!gave_up && lane == 0) mbar_arrive(&pready[tt]);
+      }
     }
     if (gave_up && lane == 0) set_error(a.err, kErrTimeout);
   } else if (warp > kTcwCopy) {
     // ---- products, issued by one thread, the tiles in turn: that keeps one tile's softmax under the other's
-    // products (with a thread for each tile the two fall into step: 4650 cycles a pair of blocks)
+    // products (with a thread for each tile the two fall into step: 4650 cycles a pair of blocks).  This thread is
+    // what the products wait for, so it does nothing else: addresses are uniform and counted up (the whole warp
+    // loops, an elected thread issues), one wait a tile, for P and the copies together.
     const int nb = __shfl_sync(0xffffffffu, j1 - j0, 0), nt = __shfl_sync(0xffffffffu, ntile, 0);  // uniform
     if (nb > 0) {
       constexpr uint32_t idesc_s = umma_idesc_bf16_f32(128, 128);
       constexpr uint32_t idesc_o = umma_idesc_bf16_f32(128, 128) | (1u << 16);  // B: channels contiguous
-      auto logits = [&](int tt, int slot) {
-        const uint32_t q = sbase + kTcwQ + tt * 32768, k = sbase + kTcwRing + slot * 32768;
+      constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // descriptors' high words: SBO, version, swizzle
+      const uint32_t q_lo = ((sbase + kTcwQ) >> 4) | (1u << 16), ring = (sbase + kTcwRing) >> 4;
+      auto logits = [&](int tt, uint32_t slot) {
+        const uint32_t k_lo = (ring + slot * 2048u) | (1u << 16);
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const uint32_t off = (s >> 2) * 16384 + (s & 3) * 32;
-          umma_f16(kTmS + tt * 128, umma_desc_sw128(q + off), umma_desc_sw128(k + off), idesc_s, s > 0);
-        }
+        for (int s = 0; s < 8; ++s)
+          umma_ss(kTmS + tt * 128, q_lo + tt * 2048 + (s >> 2) * 1024 + (s & 3) * 2, k_lo + (s >> 2) * 1024 + (s & 3) * 2, kHi,
+                  idesc_s, s > 0);
         umma_commit(&sfull[tt]);
       };
-      // (the whole warp waits and loops, so that addresses stay in uniform registers; one elected thread issues)
-      auto landed = [&](int u) {
-        return __all_sync(0xffffffffu, mbar_wait_timed(&full[u % kTcwSlots], (u / kTcwSlots) & 1, kWaitNs)) != 0;
-      };
-      bool ok = landed(0);
+      bool ok = __all_sync(0xffffffffu, mbar_wait_timed(&full[0], 0, kWaitNs));
       if (ok) {
         tc_fence_after();
         if (elect_one()) {
@@ -344,41 +362,37 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
           umma_commit(&empty[0]);
         }
         __syncwarp();
-        ok = landed(1);
       }
-      // Between a tile's products and the next one's there is nothing but the wait for P: the slots' releases and
-      // the waits for copies come behind products that are still running.
+      uint32_t sv = 1, sk = 2, phase = 0;
       for (int j = 0; j < nb && ok; ++j) {
-        const int sv = (2 * j + 1) % kTcwSlots, sk = (2 * j + 2) % kTcwSlots, before = (2 * j) % kTcwSlots;
         const bool more = j + 1 < nb;
-        for (int tt = 0; tt < nt; ++tt) {
-          ok = __all_sync(0xffffffffu, mbar_wait_timed(&pready[tt], j & 1, kWaitNs));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t v = sbase + kTcwRing + sv * 32768, tS = kTmS + tt * 128;
+        const uint32_t v_lo = (ring + sv * 2048u) | ((16384u >> 4) << 16);
 #pragma unroll
-            for (int s = 0; s < 8; ++s)  // P: keys 0-63 in S's columns 0-31, the others in 64-95
-              umma_f16_ts(kTmO + tt * 128, tS + (s >> 2) * 64 + 8 * (s & 3), umma_desc_mn_sw128(v + 2048 * s, 16384, 1024),
-                          idesc_o, j > 0 || s > 0);
-            if (!more) umma_commit(&odone[tt]);
-            if (more && tt == 0 && j > 0) umma_commit(&empty[before]);  // K_j, whose last product is behind the last V's
-            if (more && tt == nt - 1) umma_commit(&empty[sv]);
-          }
-          __syncwarp();
-          if (!more) continue;
-          if (tt == 0) {
-            ok = landed(2 * j + 2);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (elect_one()) logits(tt, sk);
-          __syncwarp();
-          if (tt == 0) {
-            ok = landed(2 * j + 3);
-            if (!ok) break;
+        for (int tt = 0; tt < 2; ++tt) {
+          if (tt < nt && ok) {
+            ok = __all_sync(0xffffffffu, mbar_wait_timed(&pready[tt], phase, kWaitNs));
+            if (ok) {
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)  // P: keys 0-63 in S's columns 0-31, the others in 64-95
+                  umma_ts(kTmO + tt * 128, kTmS + tt * 128 + (s >> 2) * 64 + 8 * (s & 3), v_lo + 128 * s, kHi, idesc_o,
+                          j > 0 || s > 0);
+                if (tt == nt - 1) umma_commit(&empty[sv]);
+                if (more) {
+                  logits(tt, sk);
+                  if (tt == nt - 1) umma_commit(&empty[sk]);
+                } else {
+                  umma_commit(&odone[tt]);
+                }
+              }
+              __syncwarp();
+            }
           }
         }
+        phase ^= 1u;
+        sv = sv + 2 >= kTcwSlots ? sv + 2 - kTcwSlots : sv + 2;
+        sk = sk + 2 >= kTcwSlots ? sk + 2 - kTcwSlots : sk + 2;
       }
       if (!ok && lane == 0) set_error(a.err, kErrTimeout);
     }
