@@ -143,6 +143,25 @@ CHUNKS = [
 ]
 
 
+MANY = [  # more work items than the GPU has SMs
+    dict(Hq=2, Hkv=1, spans=[((7 * i) % 90, 1 + i % 4, (7 * i) % 90 + 1 + i % 4) for i in range(400)], window=40, sinks=2),
+    dict(Hq=64, Hkv=8, spans=[(0, 150, 150), (300, 40, 340), (10, 131, 141), (0, 33, 33), (130, 150, 280)], window=100,
+         sinks=4),
+    dict(Hq=8, Hkv=8, spans=[(0, 200 + i, 200 + i) for i in range(0, 140, 7)], window=-1, sinks=0),
+]
+
+
+@pytest.mark.parametrize("i", range(len(MANY)))
+def test_many_work_items(i):
+    c = Case(**MANY[i], int4=False, seed=200 + i)
+    c.check()
+    first = c.out.clone()
+    c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(first, c.out)
+    c.close()
+
+
 @pytest.mark.parametrize("int4", [False, True])
 @pytest.mark.parametrize("i", range(len(SINGLE)))
 def test_single_tokens(i, int4):
