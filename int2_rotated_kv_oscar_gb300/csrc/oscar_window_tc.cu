@@ -63,8 +63,27 @@ constexpr uint32_t kTmS = 0, kTmO = 256;         // TMEM columns of S and O, 128
 constexpr float kTopSum = 1099511627776.0f;
 constexpr int kRowFloats = kD + 2;               // of a tile's record, for each of its 128 rows: O[128], m, l
 
+// x / d for 0 <= x < 2^31 by a multiplication: with d <= 2^l and mul = ceil(2^(31 + l) / d) the quotient is
+// floor(x mul / 2^(31 + l)), since x mul / 2^(31 + l) exceeds x / d by less than x / 2^(31 + l) < 1 / d.
+struct Divisor {
+  uint32_t d = 1, mul = 0x80000000u, shift = 31;
+  Divisor() = default;
+  explicit Divisor(uint32_t n) : d(n) {
+    uint32_t l = 0;
+    while ((1ull << l) < n) ++l;
+    shift = 31 + l;
+    mul = (uint32_t)(((1ull << shift) + n - 1) / n);
+  }
+  __device__ __forceinline__ int divide(int x, int& rest) const {
+    const int q = (int)(((unsigned long long)(uint32_t)x * mul) >> shift);
+    rest = x - q * (int)d;
+    return q;
+  }
+};
+
 struct TcwArgs {
   WindowLaunch a;
+  Divisor by_items, by_heads, by_batch;
   int items, tiles, qpt;  // items per (tile pair, KV head), tile pairs per request, queries per tile
   int total;              // items of the call
 };
@@ -122,6 +141,15 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
+}
+
+// 32 columns, waited for.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[2][16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[0][2]), "=r"(r[0][3]), "=r"(r[0][4]), "=r"(r[0][5]), "=r"(r[0][6]), "=r"(r[0][7]), "=r"(r[0][8]), "=r"(r[0][9]), "=r"(r[0][10]), "=r"(r[0][11]), "=r"(r[0][12]), "=r"(r[0][13]), "=r"(r[0][14]), "=r"(r[0][15]), "=r"(r[1][0]), "=r"(r[1][1]), "=r"(r[1][2]), "=r"(r[1][3]), "=r"(r[1][4]), "=r"(r[1][5]), "=r"(r[1][6]), "=r"(r[1][7]), "=r"(r[1][8]), "=r"(r[1][9]), "=r"(r[1][10]), "=r"(r[1][11]), "=r"(r[1][12]), "=r"(r[1][13]), "=r"(r[1][14]), "=r"(r[1][15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // The n lowest of 32 bits (n may lie outside 0..32).
@@ -182,21 +210,16 @@ struct TcwItem {
   int ctx, hi, lo, sinks;            // held positions; no query sees hi or beyond; windows start at lo
   PageList pl;
   int np, j0, nb;                    // pages that some query sees; the item's key blocks [j0, j0 + nb)
+  int k_clean, k_held;               // pages of the list of which some query sees every row: [k_clean, k_held)
   int k_lo, k_hi;                    // (softmax) pages of the list that every row of the tile sees whole: [k_lo, k_hi)
 };
 
 
-// False: nothing to do (the request has no such queries).  (Out of line, as are the results below: each is called
-// once an item, and what it holds in registers is not taken from the loops over key blocks, which have 96.)
-__device__ __noinline__ bool tcw_item(const TcwArgs& ta, int idx, TcwItem& t, bool report) {
+// False: nothing to do (the request has no such queries).
+__device__ __forceinline__ bool tcw_item(const TcwArgs& ta, int idx, TcwItem& t, bool report) {
   const WindowLaunch& a = ta.a;
-  int x = idx;  // later tiles (more keys) first
-  const int item = x % ta.items;
-  x /= ta.items;
-  t.h = x % a.Hkv;
-  x /= a.Hkv;
-  t.b = x % a.pages.batch;
-  const int pair = ta.tiles - 1 - x / a.pages.batch;
+  int item;  // later tiles (more keys) first
+  const int pair = ta.tiles - 1 - ta.by_batch.divide(ta.by_heads.divide(ta.by_items.divide(idx, item), t.h), t.b);
   if (!token_span(a.tok, t.b, t.p0, t.n, t.row0, a.err, report)) return false;
   t.i0 = pair * 2 * ta.qpt;
   if (t.i0 >= t.n) return false;
@@ -218,6 +241,8 @@ __device__ __noinline__ bool tcw_item(const TcwArgs& ta, int idx, TcwItem& t, bo
   t.pl.sp = t.lo > 0 ? (t.sinks + kPage - 1) / kPage : 0;
   t.pl.wb = t.lo >= t.hi ? t.pl.we : max(t.lo / kPage, t.pl.sp);
   t.np = t.pl.count();
+  t.k_clean = t.pl.sp + max(0, (t.lo + kPage - 1) / kPage - t.pl.wb);
+  t.k_held = t.pl.sp + t.hi / kPage - t.pl.wb;
   t.j0 = 0;
   t.nb = (t.np + 1) / 2;
   if (ta.items > 1) {
@@ -226,6 +251,27 @@ __device__ __noinline__ bool tcw_item(const TcwArgs& ta, int idx, TcwItem& t, bo
     t.nb = share + (item < more);
   }
   return true;
+}
+
+// First position of the k-th page of an item's list; past every position if there is none, or it is outside the pool.
+__device__ __forceinline__ int block_page(const TcwArgs& ta, const TcwItem& it, int k, bool bad) {
+  const int lp = k >= it.np ? -1 : it.pl.page(k);
+  return lp < 0 || (bad && page_of(ta.a.pages, it.b, lp, ta.a.err, false) < 0) ? INT32_MAX - 63 : lp * kPage;
+}
+
+// V rows of a block that no query of the item sees may hold anything, and 0 x NaN is not 0: they become zeros, in
+// front of the products that read them.  One warp, 16 bytes a lane: two rows of 64 channels a step.
+__device__ __noinline__ void clean_block(const TcwArgs& ta, const TcwItem& it, int k0, bool bad, uint8_t* v, int lane) {
+  const int base[2] = {block_page(ta, it, k0, bad), block_page(ta, it, k0 + 1, bad)};
+  for (int row = 0; row < 128; row += 4) {
+    const int r = row + (lane >> 3), at = (r < 64 ? base[0] : base[1]) + (r & 63);
+    if (!(at < it.hi && (at < it.sinks || at >= it.lo))) {
+      *reinterpret_cast<uint4*>(v + r * 128 + 16 * (lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(v + 16384 + r * 128 + 16 * (lane & 7)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // The records of a group's items into the result: `warps` warps, a row each.
@@ -285,7 +331,8 @@ __device__ __forceinline__ void store_rows(uint4 (&x)[8], int lane, uint32_t liv
   }
 }
 
-// This thread's half row of O, over its sum l, into the result; or, where several items share a group's keys, into
+// (Out of line, as it is called once an item: what it holds in registers is not taken from the loop over key blocks,
+// which has 96.)  This thread's half row of O, over its sum l, into the result; or, where several items share a group's keys, into
 // the group's records, which the last item joins.
 __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, uint8_t* sm, int idx, int warp, int lane,
                                         uint32_t to, bool live, bool got, float m, float l) {
@@ -475,10 +522,11 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     auto landed = [&](uint32_t u) {
       return __all_sync(0xffffffffu, mbar_wait_timed(&full[u % kTcwSlots], (u / kTcwSlots) & 1, kWaitNs)) != 0;
     };
+    // The next item is worked out for the softmax warps while they are at the result of the one before; its place is
+    // free since they came to that one.
     TcwItem* place = reinterpret_cast<TcwItem*>(sm + kTcwItems) + 2 * tt;
-    for (int idx = blockIdx.x, turn = 0; idx < ta.total; idx += gridDim.x, turn ^= 1) {
-      // the item, for the softmax warps too (while they are at the result before; the next but one comes behind
-      // another of these barriers)
+    auto put = [&](int idx, int turn) {
+      if (idx >= ta.total) return;
       if (tcw_item(ta, idx, it, false)) {
         const int tf = it.p0 + it.i0 + tt * qpt, tl = min(tf + qpt - 1, it.last);  // the tile's positions
         it.k_lo = it.pl.sp + max(0, (a.window < 0 ? 0 : max(0, tl - a.window + 1) + kPage - 1) / kPage - it.pl.wb);
@@ -488,25 +536,35 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
       }
       if (lane == 0) place[turn] = it;
       __syncwarp();
+    };
+    put(blockIdx.x, 0);
+    for (int idx = blockIdx.x, turn = 0; idx < ta.total; idx += gridDim.x, turn ^= 1) {
       group_sync(12 + tt, 288);
-      if (it.nb == 0) continue;
-      if (tt < it.ntile) {
-        for (int j = 0; j < it.nb; ++j) {
+      const TcwItem& my = place[turn];
+      const int nb = my.nb;
+      const bool active = tt < my.ntile;
+      if (active && nb > 0) {
+        for (int j = 0; j < nb; ++j) {
           if (!gave_up) gave_up = !__all_sync(0xffffffffu, mbar_wait_timed(&sfull[tt], (blocks + j) & 1, kWaitNs));
           if (gave_up && lane == 0) flags[tt] = 1;
           group_sync(9 + tt, 288);
           if (!gave_up) {
-            gave_up = !landed(use + 2 * j + 1) || (j + 1 < it.nb && !landed(use + 2 * j + 2));
+            gave_up = !landed(use + 2 * j + 1) || (j + 1 < nb && !landed(use + 2 * j + 2));
+            const bool bad = flags[2] != 0;
+            const int k0 = 2 * (my.j0 + j);
+            if (tt == 0 && !gave_up && (bad || k0 < my.k_clean || k0 + 1 >= my.k_held))
+              clean_block(ta, my, k0, bad, sm + kTcwRing + (use + 2 * j + 1) % kTcwSlots * 32768, lane);
             if (!gave_up && lane == 0) mbar_arrive(&pready[tt]);
           }
         }
         if (!gave_up) gave_up = !__all_sync(0xffffffffu, mbar_wait_timed(&odone[tt], items & 1, kWaitNs));
         if (gave_up && lane == 0) flags[tt] = 1;
         group_sync(9 + tt, 288);
-        blocks += it.nb;
+        blocks += nb;
         ++items;
       }
-      use += 2 * it.nb;
+      use += 2 * nb;
+      put(idx + gridDim.x, turn ^ 1);
     }
     if (gave_up && lane == 0) set_error(a.err, kErrTimeout);
   } else if (warp == kTcwMma) {
@@ -604,17 +662,13 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     // this row's query of the item's (-1: none)
     const int ql = 32 * (warp & 3) + lane < qpt * g ? t * qpt + (32 * (warp & 3) + lane) / g : -1;
     int round = 0;     // of the pair's votes
-    uint32_t use = 0;  // of the ring, at the item's K_0
     TcwItem* items = reinterpret_cast<TcwItem*>(sm + kTcwItems) + 2 * t;
     static_assert(4 * sizeof(TcwItem) <= kTcwX - kTcwItems, "the items' place");
     for (int idx = blockIdx.x, turn = 0; idx < ta.total; idx += gridDim.x, turn ^= 1) {
       group_sync(12 + t, 288);  // the item is there (from the relay)
       const TcwItem& my = items[turn];
       const int nb = my.nb;
-      if (t >= my.ntile) {
-        use += 2 * nb;
-        continue;
-      }
+      if (t >= my.ntile) continue;
       float m = -INFINITY, l = 0.f;
       const bool live = ql >= 0 && my.i0 + ql < my.n;
 #pragma unroll 1
@@ -630,33 +684,12 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
           const int k0 = 2 * (my.j0 + j);
           whole = k0 >= my.k_lo && k0 + 1 < my.k_hi && !any_bad;
           if (!whole) {
-            const int row = 32 * (warp & 3) + lane, np = my.np, sp = my.pl.sp, wb = my.pl.wb, hi = my.hi, sinks = my.sinks;
-            // (a page outside the pool, or none: past every position)
-            int base[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int lp = k0 + k >= np ? -1 : k0 + k < sp ? k0 + k : wb + k0 + k - sp;
-              base[k] = lp < 0 || (any_bad && page_of(a.pages, my.b, lp, a.err, false) < 0) ? INT32_MAX - 63 : lp * kPage;
-            }
-            // a V row that no query of the item sees may hold anything: it becomes zeros (by both tiles, each before
-            // its own product)
-            const int at = (row < 64 ? base[0] : base[1]) + (row & 63);
-            const bool stale = !(at < hi && (at < sinks || at >= my.lo));
-            if (__any_sync(0xffffffffu, stale) && !gave_up) {
-              const uint32_t uv = use + 2 * j + 1, sv = uv % kTcwSlots;
-              gave_up = !__all_sync(0xffffffffu, mbar_wait_timed(&full[sv], (uv / kTcwSlots) & 1, kWaitNs));
-              if (!gave_up && stale) {
-                uint8_t* v = sm + kTcwRing + sv * 32768 + hf * 16384 + row * 128;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(v + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
-            }
+            const int base = block_page(ta, my, k0 + hf, any_bad), sinks = my.sinks;
             const int p = min(my.p0 + my.i0 + max(ql, 0), my.last);
             const int lim = min(p + 1, my.ctx), low = a.window < 0 ? 0 : max(0, p - a.window + 1);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const int p32 = (hf ? base[1] : base[0]) + 32 * k;
+              const int p32 = base + 32 * k;
               seen[k] = low_bits(lim - p32) & (low_bits(sinks - p32) | ~low_bits(low - p32));
             }
           }
@@ -665,23 +698,17 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
         float2 sum = make_float2(0.f, 0.f);
         float mc = m == -INFINITY ? 0.f : m * c;
         if (!gave_up && j > 0) {
-          uint32_t s0[16], s1[16];
-          tmem_ld16_start(ts, s0);
-          tmem_ld16_wait(s0);
-          tmem_ld16_start(ts + 16, s1);
-          if (!whole) hide(s0, seen[0], 0);
-          weights(s0, c, mc, sum, w);
-          tmem_ld16_wait(s1);
-          tmem_ld16_start(ts + 32, s0);
-          if (!whole) hide(s1, seen[0], 16);
-          weights(s1, c, mc, sum, w + 8);
-          tmem_ld16_wait(s0);
-          tmem_ld16_start(ts + 48, s1);
-          if (!whole) hide(s0, seen[1], 0);
-          weights(s0, c, mc, sum, w + 16);
-          tmem_ld16_wait(s1);
-          if (!whole) hide(s1, seen[1], 16);
-          weights(s1, c, mc, sum, w + 24);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t s[2][16];
+            tmem_ld32(ts + 32 * k, s);
+            if (!whole) {
+              hide(s[0], seen[k], 0);
+              hide(s[1], seen[k], 16);
+            }
+            weights(s[0], c, mc, sum, w + 16 * k);
+            weights(s[1], c, mc, sum, w + 16 * k + 8);
+          }
         }
         // (rows that are no query's hold leftovers: they never ask)
         const bool move = live && (!(sum.x + sum.y < kTopSum) || (m == -INFINITY && (seen[0] | seen[1]) != 0));
@@ -746,7 +773,6 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
       group_sync(pair_bar, 64);
       l += __int_as_float(sm_load(theirs));
       tcw_result(ta, items[turn], sm, idx, warp, lane, to, live, !gave_up && nb > 0, m, l);
-      use += 2 * nb;
       // (the next item's products write O only once its first P is there, so after these loads)
     }
   }
@@ -809,6 +835,9 @@ cudaError_t launch_window_tc(const WindowLaunch& a, cudaStream_t stream) {
   TcwArgs ta;
   ta.a = a;
   ta.items = a.plan.items;
+  ta.by_items = Divisor(ta.items);
+  ta.by_heads = Divisor(a.Hkv);
+  ta.by_batch = Divisor(a.pages.batch);
   ta.qpt = 128 / (a.Hq / a.Hkv);
   ta.tiles = (a.tok.max_tokens + 2 * ta.qpt - 1) / (2 * ta.qpt);
   const long long total = (long long)ta.tiles * a.pages.batch * a.Hkv * ta.items;
