@@ -83,7 +83,7 @@ struct Divisor {
 
 struct TcwArgs {
   WindowLaunch a;
-  Divisor by_items, by_heads, by_batch;
+  Divisor by_items, by_heads, by_batch, by_tiles;
   int items, tiles, qpt;  // items per (tile pair, KV head), tile pairs per request, queries per tile
   int total;              // items of the call
 };
@@ -207,6 +207,7 @@ struct PageList {
 struct TcwItem {
   int b, h, row0, n, p0, i0, ntile;  // request, KV head, its tokens, the item's first query and tiles
   int last;                          // position of the item's last query
+  int record;                        // its place among the items of its (tile pair, request, KV head)
   int ctx, hi, lo, sinks;            // held positions; no query sees hi or beyond; windows start at lo
   PageList pl;
   int np, j0, nb;                    // pages that some query sees; the item's key blocks [j0, j0 + nb)
@@ -218,8 +219,16 @@ struct TcwItem {
 // False: nothing to do (the request has no such queries).
 __device__ __forceinline__ bool tcw_item(const TcwArgs& ta, int idx, TcwItem& t, bool report) {
   const WindowLaunch& a = ta.a;
-  int item;  // later tiles (more keys) first
-  const int pair = ta.tiles - 1 - ta.by_batch.divide(ta.by_heads.divide(ta.by_items.divide(idx, item), t.h), t.b);
+  int item = 0, pair;
+  if (ta.items == 1) {  // later tiles (more keys) first
+    pair = ta.tiles - 1 - ta.by_batch.divide(ta.by_heads.divide(idx, t.h), t.b);
+    t.record = idx;
+  } else {  // the tile pairs that read the same keys side by side, so that these come from memory once
+    int x = ta.by_tiles.divide(idx, pair);
+    x = ta.by_heads.divide(x, t.h);
+    t.b = ta.by_items.divide(x, item);
+    t.record = ((t.b * a.Hkv + t.h) * ta.tiles + pair) * ta.items + item;
+  }
   if (!token_span(a.tok, t.b, t.p0, t.n, t.row0, a.err, report)) return false;
   t.i0 = pair * 2 * ta.qpt;
   if (t.i0 >= t.n) return false;
@@ -283,18 +292,29 @@ __device__ __forceinline__ void tcw_join(const TcwArgs& ta, const TcwItem& it, i
   for (int rr = warp; rr < 128 * it.ntile; rr += warps) {
     const int tt = rr >> 7, r = rr & 127, q = it.i0 + tt * qpt + r / g;
     if (r >= qpt * g || q >= it.n) continue;
-    auto rec = [&](int i) { return recs + ((size_t)i * 256 + 128 * tt) * kRowFloats; };
+    const float* rec = recs + (size_t)128 * tt * kRowFloats;
+    constexpr size_t kStep = (size_t)256 * kRowFloats;  // from one item's record to the next's
     float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < ta.items; i += 32) M = fmaxf(M, __ldcg(rec(i) + 128 * kD + r));
-    M = warp_max(M);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < ta.items; ++i) {
-      const float mi = __ldcg(rec(i) + 128 * kD + r), f = mi == -INFINITY ? 0.f : exp2_t((mi - M) * c);
-      L = fmaf(__ldcg(rec(i) + 129 * kD + r), f, L);
-      // (an item without keys wrote m and l alone)
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(rec(i) + r * kD) + lane);
-      if (f > 0.f) y = make_float4(fmaf(u.x, f, y.x), fmaf(u.y, f, y.y), fmaf(u.z, f, y.z), fmaf(u.w, f, y.w));
+    for (int i0 = 0; i0 < ta.items; i0 += 32) {  // lane i: item i0 + i's maximum and sum
+      const int count = min(32, ta.items - i0);
+      const float* first = rec + i0 * kStep;
+      float m = -INFINITY, l = 0.f;
+      if (lane < count) {
+        m = __ldcg(first + lane * kStep + 128 * kD + r);
+        l = __ldcg(first + lane * kStep + 129 * kD + r);
+      }
+      const float top = fmaxf(M, warp_max(m)), down = M == -INFINITY ? 0.f : exp2_t((M - top) * c);
+      const float f = m == -INFINITY ? 0.f : exp2_t((m - top) * c);
+      M = top;
+      L = L * down + warp_sum(l * f);
+      y = make_float4(y.x * down, y.y * down, y.z * down, y.w * down);
+#pragma unroll 8
+      for (int i = 0; i < count; ++i) {  // (an item without keys wrote m and l alone)
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(first + i * kStep + r * kD) + lane);
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        if (fi > 0.f) y = make_float4(fmaf(u.x, fi, y.x), fmaf(u.y, fi, y.y), fmaf(u.z, fi, y.z), fmaf(u.w, fi, y.w));
+      }
     }
     const float f = L > 0.f ? 1.f / L : 0.f;
     reinterpret_cast<uint2*>(a.out + ((size_t)(it.row0 + q) * a.Hq + it.h * g + r % g) * kD)[lane] =
@@ -334,7 +354,7 @@ __device__ __forceinline__ void store_rows(uint4 (&x)[8], int lane, uint32_t liv
 // (Out of line, as it is called once an item: what it holds in registers is not taken from the loop over key blocks,
 // which has 96.)  This thread's half row of O, over its sum l, into the result; or, where several items share a group's keys, into
 // the group's records, which the last item joins.
-__device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, uint8_t* sm, int idx, int warp, int lane,
+__device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, uint8_t* sm, int warp, int lane,
                                         uint32_t to, bool live, bool got, float m, float l) {
   const WindowLaunch& a = ta.a;
   const int t = warp >> 3, hf = (warp >> 2) & 1, g = a.Hq / a.Hkv, qpt = ta.qpt;
@@ -363,7 +383,7 @@ __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, ui
     return;
   }
   // the records: O [row][128], then m [row], l [row]
-  float* rec = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)idx * 256 + 128 * t) * kRowFloats;
+  float* rec = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)it.record * 256 + 128 * t) * kRowFloats;
   if (live && hf == 0) {
     rec[128 * kD + row] = got ? m : -INFINITY;
     rec[129 * kD + row] = l;
@@ -385,7 +405,7 @@ __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, ui
     }
   // the last item of the group joins the records, a warp a row
   volatile int* last = reinterpret_cast<volatile int*>(sm + kTcwBars + 148);
-  const int group = idx / ta.items, threads = 256 * it.ntile;
+  const int group = it.record / ta.items, threads = 256 * it.ntile;
   __threadfence();
   group_sync(11, threads);
   if (threadIdx.x == 0) {
@@ -772,7 +792,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
       sm_store(mine, __float_as_int(l));
       group_sync(pair_bar, 64);
       l += __int_as_float(sm_load(theirs));
-      tcw_result(ta, items[turn], sm, idx, warp, lane, to, live, !gave_up && nb > 0, m, l);
+      tcw_result(ta, items[turn], sm, warp, lane, to, live, !gave_up && nb > 0, m, l);
       // (the next item's products write O only once its first P is there, so after these loads)
     }
   }
@@ -793,7 +813,7 @@ WindowPlan plan_window_tc(int64_t batch, int64_t max_tokens, int Hq, int Hkv, in
   const int qpt = 128 / (Hq / Hkv);
   const int64_t groups = batch * Hkv * ((max_tokens + 2 * qpt - 1) / (2 * qpt));
   const int64_t blocks = (max_keys + 2 * qpt + 127) / 128 + 1;
-  constexpr int kFixed = 6;
+  constexpr int kFixed = 8;
   const int64_t most = std::min<int64_t>(blocks / 2, kTcSplitBlocks * (int64_t)num_sms / std::max<int64_t>(groups, 1));
   int64_t best = INT64_MAX;
   for (int64_t n = 1; n <= std::max<int64_t>(most, 1); ++n) {
@@ -840,6 +860,7 @@ cudaError_t launch_window_tc(const WindowLaunch& a, cudaStream_t stream) {
   ta.by_batch = Divisor(a.pages.batch);
   ta.qpt = 128 / (a.Hq / a.Hkv);
   ta.tiles = (a.tok.max_tokens + 2 * ta.qpt - 1) / (2 * ta.qpt);
+  ta.by_tiles = Divisor(ta.tiles);
   const long long total = (long long)ta.tiles * a.pages.batch * a.Hkv * ta.items;
   if (total > INT32_MAX - 65536) return cudaErrorInvalidValue;
   ta.total = (int)total;
