@@ -216,11 +216,12 @@ struct TcwItem {
 };
 
 
-// False: nothing to do (the request has no such queries).
+// False: nothing to do (the request has no such queries).  SPLIT: several items share a group's keys.
+template <bool SPLIT>
 __device__ __forceinline__ bool tcw_item(const TcwArgs& ta, int idx, TcwItem& t, bool report) {
   const WindowLaunch& a = ta.a;
   int item = 0, pair;
-  if (ta.items == 1) {  // later tiles (more keys) first
+  if constexpr (!SPLIT) {  // later tiles (more keys) first
     pair = ta.tiles - 1 - ta.by_batch.divide(ta.by_heads.divide(idx, t.h), t.b);
     t.record = idx;
   } else {  // the tile pairs that read the same keys side by side, so that these come from memory once
@@ -254,7 +255,7 @@ __device__ __forceinline__ bool tcw_item(const TcwArgs& ta, int idx, TcwItem& t,
   t.k_held = t.pl.sp + t.hi / kPage - t.pl.wb;
   t.j0 = 0;
   t.nb = (t.np + 1) / 2;
-  if (ta.items > 1) {
+  if constexpr (SPLIT) {
     const int share = t.nb / ta.items, more = t.nb - share * ta.items;
     t.j0 = item * share + min(item, more);
     t.nb = share + (item < more);
@@ -354,6 +355,7 @@ __device__ __forceinline__ void store_rows(uint4 (&x)[8], int lane, uint32_t liv
 // (Out of line, as it is called once an item: what it holds in registers is not taken from the loop over key blocks,
 // which has 96.)  This thread's half row of O, over its sum l, into the result; or, where several items share a group's keys, into
 // the group's records, which the last item joins.
+template <bool SPLIT>
 __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, uint8_t* sm, int warp, int lane,
                                         uint32_t to, bool live, bool got, float m, float l) {
   const WindowLaunch& a = ta.a;
@@ -361,7 +363,7 @@ __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, ui
   const int row = 32 * (warp & 3) + lane;
   const uint32_t rows = __ballot_sync(0xffffffffu, live);
   uint4 x[8];
-  if (ta.items == 1) {
+  if constexpr (!SPLIT) {
     const float f = got && l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -380,46 +382,47 @@ __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, ui
     store_rows(x, lane, rows, [&](int r) {
       return reinterpret_cast<uint4*>(a.out + (size_t)__shfl_sync(0xffffffffu, mine, r) * kD + 64 * hf);
     });
-    return;
-  }
-  // the records: O [row][128], then m [row], l [row]
-  float* rec = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)it.record * 256 + 128 * t) * kRowFloats;
-  if (live && hf == 0) {
-    rec[128 * kD + row] = got ? m : -INFINITY;
-    rec[129 * kD + row] = l;
-  }
-  if (got)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t o[16];
-        tmem_ld16_start(to + 32 * half + 16 * k, o);
-        tmem_ld16_wait(o);
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) x[4 * k + (e >> 2)] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-      }
-      store_rows(x, lane, rows, [&](int r) {
-        return reinterpret_cast<uint4*>(rec + (32 * (warp & 3) + r) * kD + 64 * hf + 32 * half);
-      });
+  } else {
+    // the records: O [row][128], then m [row], l [row]
+    float* rec = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)it.record * 256 + 128 * t) * kRowFloats;
+    if (live && hf == 0) {
+      rec[128 * kD + row] = got ? m : -INFINITY;
+      rec[129 * kD + row] = l;
     }
-  // the last item of the group joins the records, a warp a row
-  volatile int* last = reinterpret_cast<volatile int*>(sm + kTcwBars + 148);
-  const int group = it.record / ta.items, threads = 256 * it.ntile;
-  __threadfence();
-  group_sync(11, threads);
-  if (threadIdx.x == 0) {
-    unsigned* counter = reinterpret_cast<unsigned*>(a.workspace) + group;
-    *last = atomicAdd(counter, 1u) == (unsigned)ta.items - 1u;
-    if (*last) *counter = 0u;
-  }
-  group_sync(11, threads);
-  if (*last) {
+    if (got)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t o[16];
+          tmem_ld16_start(to + 32 * half + 16 * k, o);
+          tmem_ld16_wait(o);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) x[4 * k + (e >> 2)] = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+        store_rows(x, lane, rows, [&](int r) {
+          return reinterpret_cast<uint4*>(rec + (32 * (warp & 3) + r) * kD + 64 * hf + 32 * half);
+        });
+      }
+    // the last item of the group joins the records, a warp a row
+    volatile int* last = reinterpret_cast<volatile int*>(sm + kTcwBars + 148);
+    const int group = it.record / ta.items, threads = 256 * it.ntile;
     __threadfence();
-    tcw_join(ta, it, group, warp, threads / 32, lane);
+    group_sync(11, threads);
+    if (threadIdx.x == 0) {
+      unsigned* counter = reinterpret_cast<unsigned*>(a.workspace) + group;
+      *last = atomicAdd(counter, 1u) == (unsigned)ta.items - 1u;
+      if (*last) *counter = 0u;
+    }
+    group_sync(11, threads);
+    if (*last) {
+      __threadfence();
+      tcw_join(ta, it, group, warp, threads / 32, lane);
+    }
   }
 }
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kTcwThreads, 1)
     window_tc_kernel(const __grid_constant__ TcwArgs ta, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     // ---- copies: an item's use 0 of the ring is K_0, 2 j + 1 is V_j, 2 j + 2 is K_(j + 1)
     uint32_t use = 0, items = 0;
     for (int idx = blockIdx.x; idx < ta.total && !gave_up; idx += gridDim.x) {
-      if (!tcw_item(ta, idx, it, lane == 0) || it.nb == 0) continue;
+      if (!tcw_item<SPLIT>(ta, idx, it, lane == 0) || it.nb == 0) continue;
       int phys_l = -1, fetched = 0;
       auto phys_of = [&](int k) {  // k-th page of this item (whole warp)
         if (k >= fetched) {
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     TcwItem* place = reinterpret_cast<TcwItem*>(sm + kTcwItems) + 2 * tt;
     auto put = [&](int idx, int turn) {
       if (idx >= ta.total) return;
-      if (tcw_item(ta, idx, it, false)) {
+      if (tcw_item<SPLIT>(ta, idx, it, false)) {
         const int tf = it.p0 + it.i0 + tt * qpt, tl = min(tf + qpt - 1, it.last);  // the tile's positions
         it.k_lo = it.pl.sp + max(0, (a.window < 0 ? 0 : max(0, tl - a.window + 1) + kPage - 1) / kPage - it.pl.wb);
         it.k_hi = it.pl.sp + min(tf + 1, it.ctx) / kPage - it.pl.wb;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
     bool ok = true;
     int idx = blockIdx.x;
     auto next_item = [&]() {  // to the next item with work, from idx on
-      while (idx < ta.total && (!tcw_item(ta, idx, it, false) || it.nb == 0)) idx += gridDim.x;
+      while (idx < ta.total && (!tcw_item<SPLIT>(ta, idx, it, false) || it.nb == 0)) idx += gridDim.x;
       return idx < ta.total;
     };
     bool have = next_item();
@@ -792,7 +795,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
       sm_store(mine, __float_as_int(l));
       group_sync(pair_bar, 64);
       l += __int_as_float(sm_load(theirs));
-      tcw_result(ta, items[turn], sm, warp, lane, to, live, !gave_up && nb > 0, m, l);
+      tcw_result<SPLIT>(ta, items[turn], sm, warp, lane, to, live, !gave_up && nb > 0, m, l);
       // (the next item's products write O only once its first P is there, so after these loads)
     }
   }
@@ -830,8 +833,10 @@ WindowPlan plan_window_tc(int64_t batch, int64_t max_tokens, int Hq, int Hkv, in
 }
 
 cudaError_t launch_window_tc(const WindowLaunch& a, cudaStream_t stream) {
-  static std::atomic<uint64_t> done;
-  const cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(window_tc_kernel), kTcwSmem, done);
+  static std::atomic<uint64_t> done[2];
+  const bool split = a.plan.items > 1;
+  const void* fn = split ? reinterpret_cast<const void*>(window_tc_kernel<true>) : reinterpret_cast<const void*>(window_tc_kernel<false>);
+  const cudaError_t e = smem_attr_once(fn, kTcwSmem, done[split]);
   if (e != cudaSuccess) return e;
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
     void* fn = nullptr;
@@ -874,7 +879,7 @@ cudaError_t launch_window_tc(const WindowLaunch& a, cudaStream_t stream) {
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
   void* args[] = {&ta, &tm[0], &tm[1], &tm[2]};
-  return launch_pdl(reinterpret_cast<const void*>(window_tc_kernel), dim3((unsigned)std::min<long long>(total, std::max(a.num_sms, 1))),
+  return launch_pdl(fn, dim3((unsigned)std::min<long long>(total, std::max(a.num_sms, 1))),
                     dim3(kTcwThreads), kTcwSmem, stream, args);
 }
 
