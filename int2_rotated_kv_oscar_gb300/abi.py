@@ -168,6 +168,8 @@ def library_path():
 def load(build_if_missing=True):
     """Load (building first if needed) the shared library; raises if that is impossible."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -25,7 +25,10 @@ struct DeviceGuard {
   int prev = -1;
   explicit DeviceGuard(int dev) {
     if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != dev) cudaSetDevice(dev);
+    if (prev != dev)
+      cudaSetDevice(dev);
+    else
+      prev = -1;  // nothing to put back
   }
   ~DeviceGuard() {
     if (prev >= 0) cudaSetDevice(prev);

@@ -44,33 +44,35 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// x c - y s with each product and the difference rounded once, as written: a fused product would round the
-// two terms differently, and its bits would not be those of the formula in elementary operations.
-__device__ __forceinline__ float turned(float x, float c, float y, float s) {
-  return __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-}
-__device__ __forceinline__ float turned_back(float y, float c, float x, float s) {
-  return __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+// (x c - y s, y c + x s) for two pairs at once, each product and sum rounded once, as written: a fused product would
+// round the two terms differently, and its bits would not be those of the formula in elementary operations.
+__device__ __forceinline__ void turn2(float2& x, float2& y, float2 c, float2 s) {
+  const float2 z = make_float2(-y.x, -y.y), u = fadd2(fmul2(x, c), fmul2(z, s));
+  y = fadd2(fmul2(y, c), fmul2(x, s));
+  x = u;
 }
 
 // Turn eight pairs: a = (x0..x7), b = (y0..y7) as bf16, c and s their cosines and sines.
 __device__ __forceinline__ void turn8(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t ua = word_of(a, i), ub = word_of(b, i);
-    const float x0 = bf16_lo(ua), x1 = bf16_hi(ua), y0 = bf16_lo(ub), y1 = bf16_hi(ub);
-    word_of(a, i) = pack_bf16x2(turned(x0, c[2 * i], y0, s[2 * i]), turned(x1, c[2 * i + 1], y1, s[2 * i + 1]));
-    word_of(b, i) = pack_bf16x2(turned_back(y0, c[2 * i], x0, s[2 * i]), turned_back(y1, c[2 * i + 1], x1, s[2 * i + 1]));
+    float2 x = make_float2(bf16_lo(word_of(a, i)), bf16_hi(word_of(a, i)));
+    float2 y = make_float2(bf16_lo(word_of(b, i)), bf16_hi(word_of(b, i)));
+    turn2(x, y, make_float2(c[2 * i], c[2 * i + 1]), make_float2(s[2 * i], s[2 * i + 1]));
+    word_of(a, i) = pack_bf16x2(x.x, x.y);
+    word_of(b, i) = pack_bf16x2(y.x, y.y);
   }
 }
 
 // Turn four adjacent pairs held in one 16-byte piece.
 __device__ __forceinline__ void turn4(uint4& a, const float* c, const float* s) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = word_of(a, i);
-    const float x = bf16_lo(u), y = bf16_hi(u);
-    word_of(a, i) = pack_bf16x2(turned(x, c[i], y, s[i]), turned_back(y, c[i], x, s[i]));
+  for (int i = 0; i < 4; i += 2) {
+    float2 x = make_float2(bf16_lo(word_of(a, i)), bf16_lo(word_of(a, i + 1)));
+    float2 y = make_float2(bf16_hi(word_of(a, i)), bf16_hi(word_of(a, i + 1)));
+    turn2(x, y, make_float2(c[i], c[i + 1]), make_float2(s[i], s[i + 1]));
+    word_of(a, i) = pack_bf16x2(x.x, y.x);
+    word_of(a, i + 1) = pack_bf16x2(x.y, y.y);
   }
 }
 
