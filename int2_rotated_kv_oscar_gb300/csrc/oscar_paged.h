@@ -79,11 +79,13 @@ struct WindowLaunch {
   int32_t num_sms = 0;
   unsigned* err = nullptr;
 };
+constexpr int kCutBlocks = 2;  // blocks (split kernel) or items (tensor-core kernel) per SM that share out keys, at most
+inline size_t window_counter_bytes(int num_sms) { return ((size_t)kCutBlocks * num_sms * sizeof(unsigned) + 255) & ~(size_t)255; }
 WindowPlan plan_window(bool int4, int64_t rows, int Hq, int Hkv, int64_t max_keys, int num_sms);
 cudaError_t launch_window_split(const WindowLaunch& a, cudaStream_t stream);
 
-// Chunks and prompts over BF16 pages, on the tensor cores (records [blocks][256 rows][130] of its items).
-constexpr int kTcSplitBlocks = 2;  // blocks per SM that one call may split its keys over
+// Chunks and prompts over BF16 pages, on the tensor cores (records [items][256 rows][130])
+// (the counters are the split kernel's; this one keeps off them)
 WindowPlan plan_window_tc(int64_t batch, int64_t max_tokens, int Hq, int Hkv, int64_t max_keys, int num_sms);
 cudaError_t launch_window_tc(const WindowLaunch& a, cudaStream_t stream);
 

@@ -846,8 +846,9 @@ WindowPlan plan_window(bool int4, int64_t rows, int Hq, int Hkv, int64_t max_key
             : !int4               ? blocks_of<false, true>(units, num_sms)
             : wide(rows, Hkv)     ? blocks_of<true, true>(units, num_sms)
                                   : blocks_of<true, false>(units, num_sms);
-  const int64_t most = (int64_t)Ring<true, false>::kBlocks * num_sms;  // blocks of any call
-  p.off_records = ((size_t)most * sizeof(unsigned) + 255) & ~(size_t)255;
+  static_assert(Ring<true, false>::kBlocks == kCutBlocks && Ring<true, true>::kBlocks <= kCutBlocks && Ring<false, true>::kBlocks <= kCutBlocks);
+  const int64_t most = (int64_t)kCutBlocks * num_sms;  // blocks of any call
+  p.off_records = window_counter_bytes(num_sms);
   p.total = p.off_records + (size_t)most * 2 * ((Hq / Hkv) * (kD + 2) + 3) * sizeof(float);
   return p;
 }

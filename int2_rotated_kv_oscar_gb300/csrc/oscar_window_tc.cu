@@ -30,8 +30,8 @@
 // result of the one before are still under way (a block per item: 25,000 of
 // 105,000 cycles an item were its beginning and its end).  An item sees only
 // the pages that some of its queries see.  With few (tile pair, KV head) groups
-// their keys are split over several items, whose records (m, l, O) the last one
-// to finish joins in item order.
+// their keys are split over several items, whose records (m, l, O) a second
+// kernel joins in item order.
 
 #include "oscar_paged.cuh"
 
@@ -284,45 +284,6 @@ __device__ __noinline__ void clean_block(const TcwArgs& ta, const TcwItem& it, i
   __syncwarp();
 }
 
-// The records of a group's items into the result: `warps` warps, a row each.
-__device__ __forceinline__ void tcw_join(const TcwArgs& ta, const TcwItem& it, int group, int warp, int warps, int lane) {
-  const WindowLaunch& a = ta.a;
-  const int g = a.Hq / a.Hkv, qpt = ta.qpt;
-  const float c = a.sm_scale * kLog2eT;
-  const float* recs = reinterpret_cast<const float*>(a.workspace + a.plan.off_records) + (size_t)group * ta.items * 256 * kRowFloats;
-  for (int rr = warp; rr < 128 * it.ntile; rr += warps) {
-    const int tt = rr >> 7, r = rr & 127, q = it.i0 + tt * qpt + r / g;
-    if (r >= qpt * g || q >= it.n) continue;
-    const float* rec = recs + (size_t)128 * tt * kRowFloats;
-    constexpr size_t kStep = (size_t)256 * kRowFloats;  // from one item's record to the next's
-    float M = -INFINITY, L = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < ta.items; i0 += 32) {  // lane i: item i0 + i's maximum and sum
-      const int count = min(32, ta.items - i0);
-      const float* first = rec + i0 * kStep;
-      float m = -INFINITY, l = 0.f;
-      if (lane < count) {
-        m = __ldcg(first + lane * kStep + 128 * kD + r);
-        l = __ldcg(first + lane * kStep + 129 * kD + r);
-      }
-      const float top = fmaxf(M, warp_max(m)), down = M == -INFINITY ? 0.f : exp2_t((M - top) * c);
-      const float f = m == -INFINITY ? 0.f : exp2_t((m - top) * c);
-      M = top;
-      L = L * down + warp_sum(l * f);
-      y = make_float4(y.x * down, y.y * down, y.z * down, y.w * down);
-#pragma unroll 8
-      for (int i = 0; i < count; ++i) {  // (an item without keys wrote m and l alone)
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(first + i * kStep + r * kD) + lane);
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        if (fi > 0.f) y = make_float4(fmaf(u.x, fi, y.x), fmaf(u.y, fi, y.y), fmaf(u.z, fi, y.z), fmaf(u.w, fi, y.w));
-      }
-    }
-    const float f = L > 0.f ? 1.f / L : 0.f;
-    reinterpret_cast<uint2*>(a.out + ((size_t)(it.row0 + q) * a.Hq + it.h * g + r % g) * kD)[lane] =
-        make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-  }
-}
-
 // Eight 16-byte pieces of each lane's row to memory: an 8 x 8 exchange among eight lanes first, so that they write
 // 128 contiguous bytes of a row (each lane its own row took 12,000 cycles a tile).  at(r): where row r (0..31 of
 // the warp) has them; `live`: the warp's rows that are written.
@@ -353,8 +314,8 @@ __device__ __forceinline__ void store_rows(uint4 (&x)[8], int lane, uint32_t liv
 }
 
 // (Out of line, as it is called once an item: what it holds in registers is not taken from the loop over key blocks,
-// which has 96.)  This thread's half row of O, over its sum l, into the result; or, where several items share a group's keys, into
-// the group's records, which the last item joins.
+// which has 96.)  This thread's half row of O, over its sum l, into the result; or, where several items share a group's
+// keys, into the group's records, which window_join_kernel joins.
 template <bool SPLIT>
 __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, uint8_t* sm, int warp, int lane,
                                         uint32_t to, bool live, bool got, float m, float l) {
@@ -404,21 +365,6 @@ __device__ __noinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it, ui
           return reinterpret_cast<uint4*>(rec + (32 * (warp & 3) + r) * kD + 64 * hf + 32 * half);
         });
       }
-    // the last item of the group joins the records, a warp a row
-    volatile int* last = reinterpret_cast<volatile int*>(sm + kTcwBars + 148);
-    const int group = it.record / ta.items, threads = 256 * it.ntile;
-    __threadfence();
-    group_sync(11, threads);
-    if (threadIdx.x == 0) {
-      unsigned* counter = reinterpret_cast<unsigned*>(a.workspace) + group;
-      *last = atomicAdd(counter, 1u) == (unsigned)ta.items - 1u;
-      if (*last) *counter = 0u;
-    }
-    group_sync(11, threads);
-    if (*last) {
-      __threadfence();
-      tcw_join(ta, it, group, warp, threads / 32, lane);
-    }
   }
 }
 
@@ -440,7 +386,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
   uint64_t* qfull = odone + 2;                                  // the item's queries landed
   uint64_t* qempty = qfull + 1;                                 // read by the item's last logits
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(qempty + 1);
-  volatile int* flags = reinterpret_cast<volatile int*>(tmem_at + 2);  // (behind the join's word)
+  volatile int* flags = reinterpret_cast<volatile int*>(tmem_at + 2);
   // [0, 1] the relay of tile t gave up; [2] a page outside the pool was met
   int* words = reinterpret_cast<int*>(sm + kTcwBars + 192);     // [8] the pairs' words
   griddep_launch_dependents();
@@ -807,6 +753,51 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
   }
 }
 
+// The records of each group's items into the result, in item order: a warp a row.  A kernel of its own, so that all
+// SMs have a part in it: with the last item of each group joining the rest, 32 tokens at 4096 of one request took 72 us,
+// now 18; 256 at 100,000 329 us, now 300.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_constant__ TcwArgs ta) {
+  griddep_launch_dependents();
+  const WindowLaunch& a = ta.a;
+  const int g = a.Hq / a.Hkv, lane = threadIdx.x & 31, i = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int q = i / g, head = i - q * g;  // the row's query among its tile pair's, and its query head
+  int pair, h, p0, n, row0;
+  const int b = ta.by_heads.divide(ta.by_tiles.divide((int)blockIdx.y, pair), h);
+  griddep_wait();
+  if (!token_span(a.tok, b, p0, n, row0, a.err, false) || q >= 2 * ta.qpt || pair * 2 * ta.qpt + q >= n) return;
+  const int tt = q >= ta.qpt, r = (q - tt * ta.qpt) * g + head;
+  const float c = a.sm_scale * kLog2eT;
+  constexpr size_t kStep = (size_t)256 * kRowFloats;  // from one item's record to the next's
+  const float* rec = reinterpret_cast<const float*>(a.workspace + a.plan.off_records) +
+                     (size_t)((b * a.Hkv + h) * ta.tiles + pair) * ta.items * kStep + (size_t)128 * tt * kRowFloats;
+  float M = -INFINITY, L = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < ta.items; i0 += 32) {  // lane i: item i0 + i's maximum and sum
+    const int count = min(32, ta.items - i0);
+    const float* first = rec + i0 * kStep;
+    float m = -INFINITY, l = 0.f;
+    if (lane < count) {
+      m = __ldcg(first + lane * kStep + 128 * kD + r);
+      l = __ldcg(first + lane * kStep + 129 * kD + r);
+    }
+    const float top = fmaxf(M, warp_max(m)), down = M == -INFINITY ? 0.f : exp2_t((M - top) * c);
+    const float f = m == -INFINITY ? 0.f : exp2_t((m - top) * c);
+    M = top;
+    L = L * down + warp_sum(l * f);
+    y = make_float4(y.x * down, y.y * down, y.z * down, y.w * down);
+#pragma unroll 8
+    for (int k = 0; k < count; ++k) {  // (an item without keys wrote m and l alone)
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(first + k * kStep + r * kD) + lane);
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      if (fk > 0.f) y = make_float4(fmaf(u.x, fk, y.x), fmaf(u.y, fk, y.y), fmaf(u.z, fk, y.z), fmaf(u.w, fk, y.w));
+    }
+  }
+  const float f = L > 0.f ? 1.f / L : 0.f;
+  reinterpret_cast<uint2*>(a.out + ((size_t)(row0 + pair * 2 * ta.qpt + q) * a.Hq + h * g + head) * kD)[lane] =
+      make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+}
+
 }  // namespace
 
 // Items per (tile pair, KV head): the fewest rounds of the grid times an item's length in key blocks (plus a
@@ -817,7 +808,7 @@ WindowPlan plan_window_tc(int64_t batch, int64_t max_tokens, int Hq, int Hkv, in
   const int64_t groups = batch * Hkv * ((max_tokens + 2 * qpt - 1) / (2 * qpt));
   const int64_t blocks = (max_keys + 2 * qpt + 127) / 128 + 1;
   constexpr int kFixed = 8;
-  const int64_t most = std::min<int64_t>(blocks / 2, kTcSplitBlocks * (int64_t)num_sms / std::max<int64_t>(groups, 1));
+  const int64_t most = std::min<int64_t>(blocks / 2, kCutBlocks * (int64_t)num_sms / std::max<int64_t>(groups, 1));
   int64_t best = INT64_MAX;
   for (int64_t n = 1; n <= std::max<int64_t>(most, 1); ++n) {
     const int64_t waves = (groups * n + num_sms - 1) / std::max(num_sms, 1);
@@ -827,8 +818,8 @@ WindowPlan plan_window_tc(int64_t batch, int64_t max_tokens, int Hq, int Hkv, in
       p.items = (int)n;
     }
   }
-  p.off_records = ((size_t)kTcSplitBlocks * num_sms * sizeof(unsigned) + 255) & ~(size_t)255;
-  p.total = p.off_records + (size_t)kTcSplitBlocks * num_sms * 256 * kRowFloats * sizeof(float);
+  p.off_records = window_counter_bytes(num_sms);
+  p.total = p.off_records + (size_t)kCutBlocks * num_sms * 256 * kRowFloats * sizeof(float);
   return p;
 }
 
@@ -879,8 +870,13 @@ cudaError_t launch_window_tc(const WindowLaunch& a, cudaStream_t stream) {
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
   void* args[] = {&ta, &tm[0], &tm[1], &tm[2]};
-  return launch_pdl(fn, dim3((unsigned)std::min<long long>(total, std::max(a.num_sms, 1))),
-                    dim3(kTcwThreads), kTcwSmem, stream, args);
+  const cudaError_t r = launch_pdl(fn, dim3((unsigned)std::min<long long>(total, std::max(a.num_sms, 1))),
+                                   dim3(kTcwThreads), kTcwSmem, stream, args);
+  if (r != cudaSuccess || !split) return r;
+  const int rows = std::min(a.tok.max_tokens, 2 * ta.qpt) * (a.Hq / a.Hkv);
+  return launch_pdl(reinterpret_cast<const void*>(window_join_kernel),
+                    dim3((unsigned)(rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), (unsigned)(total / ta.items)),
+                    dim3(kJoinThreads), 0, stream, args);
 }
 
 }  // namespace oscar
