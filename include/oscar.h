@@ -573,14 +573,19 @@ oscar_status oscar_int4_to_bf16(oscar_ctx* ctx, const oscar_int4_cache_view* fro
  *   ctx_len  device int32 [batch]: positions that the cache holds (below
  *            them every visible position's page must be in the table).
  *   max_ctx_len  host upper bound of ctx_len (sizes the launch; a larger
- *            ctx_len is still attended, only less evenly split).
+ *            ctx_len is still attended, only less evenly split; but a
+ *            single token's or the 4-bit cache's, with more than 2^30 /
+ *            (n_tokens num_kv_heads) tiles of 16 visible, sets
+ *            OSCAR_DEVERR_LENGTH and gets zeros).
  *   window   visible positions up to the query's own; negative: all of them;
  *            0: the sinks alone.
  *   sinks    first positions that stay visible (>= 0).
  *   sm_scale softmax scale; <= 0 selects 1/sqrt(128).
  * Cache rows that no query of the call sees may hold anything, NaN included.
  * A V row that is not finite may reach, beside the queries that see it, others
- * of its request (their tile of 128 rows).
+ * of its request (their tile of 128 rows).  The sums may run up to 2^50 times
+ * larger than the result before their division, so values of V beyond 2^77
+ * may overflow.
  */
 typedef struct {
   const void* q;

@@ -146,6 +146,7 @@ __device__ __forceinline__ bool seen_by(const WindowLaunch& a, int i, int& b, Se
 struct WindowArgs {
   WindowLaunch a;
   bool cut;  // the pairs' units are cut into equal ranges (else a block a pair)
+  int most;  // cut: units of a row, at most, so that all of them stay below 2^30 whatever the lengths on the device
 };
 
 // Copy unit `t0` (tile index in the list) of the query's keys into a stage.  BF16: rows of 256 bytes,
@@ -250,8 +251,13 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   if (wa.cut) {
     int b;
     Seen s;
+    auto units_of = [&](int i, bool report) {  // (far more than the host's bound allows: nothing, and an error)
+      const int n = seen_by<KU>(a, i, b, s, report) ? s.tiles() / KU : 0;
+      if (n > wa.most && report) set_error(a.err, kErrLength);
+      return n > wa.most ? 0 : n;
+    };
     if (few) {
-      if (lane < rows && seen_by<KU>(a, lane, b, s, block == 0 && warp == 0)) units_l = s.tiles() / KU;
+      if (lane < rows) units_l = units_of(lane, block == 0 && warp == 0);
       pre_l = units_l;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -268,7 +274,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         n[i] = 0;
-        if (i < per && first + i < rows && seen_by<KU>(a, first + i, b, s, block == 0)) n[i] = s.tiles() / KU;
+        if (i < per && first + i < rows) n[i] = units_of(first + i, block == 0);
         sum += n[i];
       }
       int inc = sum;
@@ -820,6 +826,7 @@ cudaError_t launch_one(const WindowLaunch& a, cudaStream_t stream) {
   WindowArgs wa;
   wa.a = a;
   wa.cut = a.plan.items > 0;
+  wa.most = wa.cut ? (1 << 30) / (a.tok.n_tokens * a.Hkv) : 0;
   const long long blocks = wa.cut ? a.plan.items : (long long)a.tok.n_tokens * a.Hkv;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   void* args[] = {&wa};
