@@ -49,7 +49,7 @@ cudaError_t launch_rope_table(float* table, int32_t n_positions, int32_t rotary,
 struct Read4Launch {
   PageRefs from, to;
   const int32_t *pos = nullptr, *count = nullptr;
-  int32_t max_count = 0, Hkv = 0;
+  int32_t max_count = 0, Hkv = 0, num_sms = 0;
   const uint8_t* pages4 = nullptr;
   uint16_t *k_pages = nullptr, *v_pages = nullptr;
   unsigned* err = nullptr;

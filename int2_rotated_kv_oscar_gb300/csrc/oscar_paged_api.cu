@@ -197,6 +197,7 @@ oscar_status oscar_int4_to_bf16(oscar_ctx* ctx, const oscar_int4_cache_view* fro
   a.count = count;
   a.max_count = max_count;
   a.Hkv = ctx->cfg.num_kv_heads;
+  a.num_sms = ctx->num_sms;
   a.pages4 = static_cast<const uint8_t*>(from->pages);
   a.k_pages = static_cast<uint16_t*>(const_cast<void*>(to->k_pages));
   a.v_pages = static_cast<uint16_t*>(const_cast<void*>(to->v_pages));

@@ -159,9 +159,12 @@ constexpr uint32_t kMagic4Bits = 0x4B400000u;
 // quotient may leave 0..15 (a subnormal scale's rounding, or a scale cut at fp16's largest).
 __device__ __forceinline__ __half scale4(float m, float& inv, bool& clips) {
   const float a = fminf(m * kInvSqrt128, kMaxScale4 * 7.5f);
-  const __half h = __float2half_rn(a / 7.5f);
+  // a / 7.5: the product with 1 / 7.5, and what it lacks once more (the quotient to half a step of fp32)
+  float q = a * (1.f / 7.5f);
+  q = fmaf(fmaf(-7.5f, q, a), 1.f / 7.5f, q);
+  const __half h = __float2half_rn(q);
   const float s = __half2float(h);
-  inv = s > 0.f ? kInvSqrt128 / s : 0.f;
+  inv = s > 0.f ? __fdividef(kInvSqrt128, s) : 0.f;  // (two steps of fp32, as the sums' own roundings)
   clips = clips || s < 6.2e-5f || m * kInvSqrt128 > kMaxScale4 * 7.5f;
   return h;
 }
@@ -222,12 +225,13 @@ __device__ __forceinline__ float max4(float m, float2 a, float2 b) {
   return fmaxf(fmaxf(m, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
 }
 
+// A warp's `per` heads (of K's, then V's) of one tile: the next head's rows are on their way while one is turned and
+// rounded.  `sm`: 8 KB of the warp's own, two heads' rows, each lane's 16-byte pieces read by that lane alone.
 template <int TURN>
-__device__ __forceinline__ void append_tile4(const RopeLaunch& a, int unit, int b) {
+__device__ __forceinline__ void append_tiles4(const RopeLaunch& a, int unit, int b, int per, uint32_t sm) {
   const int lane = threadIdx.x & 31, r = lane >> 2, tq = lane & 3;
-  const int head = unit % (2 * a.Hkv), tile = unit / (2 * a.Hkv);
-  const bool is_v = head >= a.Hkv;
-  const int h = is_v ? head - a.Hkv : head;
+  const int groups = (2 * a.Hkv + per - 1) / per, tile = unit / groups;
+  const int first = (unit - tile * groups) * per, last = min(first + per, 2 * a.Hkv);
   int p0, n, row0;
   if (!token_span(a.tok, b, p0, n, row0, a.err, lane == 0)) return;
   const int T = (max(p0, 0) >> 4) + tile;
@@ -243,16 +247,33 @@ __device__ __forceinline__ void append_tile4(const RopeLaunch& a, int unit, int 
   const int phys = page_of(a.pages, b, T >> 2, a.err, lane == 0);
   if (phys < 0) return;
   const bool v0 = r >= lo && r < hi, v1 = r + 8 >= lo && r + 8 < hi;
-  Tile4 t;
-  const uint16_t* x = is_v ? a.v : a.k;
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const long long tok = (long long)row0 + (base - p0) + r;
+  sm += 16 * lane;
+  auto load = [&](int head) {
+    const bool is_v = head >= a.Hkv;
+    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+    const uint16_t* x = (is_v ? a.v + (size_t)(head - a.Hkv) * kD : a.k + (size_t)head * kD) + 8 * tq;
+    const uint16_t* x0 = v0 ? x + tok * stride : x;
+    const uint16_t* x1 = v1 ? x + (tok + 8) * stride : x;
+    const uint32_t dst = sm + 4096 * (head & 1);
 #pragma unroll
-  for (int rh = 0; rh < 2; ++rh)
+    for (int M = 0; M < 4; ++M) {
+      cp_async16(dst + 512 * M, x0 + 32 * M, v0);
+      cp_async16(dst + 512 * (4 + M), x1 + 32 * M, v1);
+    }
+  };
+  load(first);
+  cp_async_commit();
+#pragma unroll 1
+  for (int head = first; head < last; ++head) {
+  if (head + 1 < last) load(head + 1);
+  cp_async_commit();
+  cp_async_wait<1>();
+  const bool is_v = head >= a.Hkv;
+  const int h = is_v ? head - a.Hkv : head;
+  Tile4 t;
 #pragma unroll
-    for (int M = 0; M < 4; ++M)
-      t.x[rh][M] = (rh ? v1 : v0) ? reinterpret_cast<const uint4*>(x + (tok + 8 * rh) * stride + (size_t)h * kD)[tq + 4 * M]
-                                  : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < 8; ++i) t.x[i >> 2][i & 3] = lds128(sm + 4096 * (head & 1) + 512 * i);
   if constexpr (TURN != kTurnNone)
     if (!is_v) turn_tile<TURN>(t, a, (int)base + r, v0, v1, tq);
   uint8_t* blk = a.pages4 + ((size_t)phys * a.Hkv + h) * kBlock4Bytes + (size_t)(T & 3) * kTile4Bytes;
@@ -372,21 +393,21 @@ __device__ __forceinline__ void append_tile4(const RopeLaunch& a, int unit, int 
         if (u >= lo && u < hi) *reinterpret_cast<__half2*>(blk + kTile4Scales + 64 + 4 * u) = sc[q & 1][q >> 1];
       }
   }
+  }
 }
 
 template <int TURN>
-// (blocks of 4 warps and 80 registers: 24 warps on an SM hide the loads' latency; 131,072 tokens x 8 heads of K and
-// V: 200 us, 216 with blocks of 8 warps, 220 with 104 registers)
-__global__ void __launch_bounds__(128, 6) rope_append_int4_kernel(const __grid_constant__ RopeLaunch a, int kv_blocks,
-                                                               int units, int split) {
+__global__ void __launch_bounds__(128, 4) rope_append_int4_kernel(const __grid_constant__ RopeLaunch a, int kv_blocks,
+                                                               int units, int per, int split) {
+  extern __shared__ __align__(16) uint8_t sm[];
   griddep_launch_dependents();
   griddep_wait();
   if ((int)blockIdx.x >= kv_blocks) {  // the queries' rows
     rope_rows<TURN, false, 128>(a, blockIdx.x - kv_blocks, blockIdx.y, split);
     return;
   }
-  const int unit = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (unit < units) append_tile4<TURN>(a, unit, blockIdx.y);
+  const int warp = threadIdx.x >> 5, unit = blockIdx.x * 4 + warp;
+  if (unit < units) append_tiles4<TURN>(a, unit, blockIdx.y, per, smem_u32(sm) + 8192 * warp);
 }
 
 // ---------------------------------------------------------------- reading the 4-bit cache back
@@ -408,15 +429,15 @@ __device__ __forceinline__ uint32_t signs_f16(int lo, int hi) {
 
 // The transform back: the levels of 16 tokens as the MMA's rows (exact in fp16), the stages over bits
 // 2 and 5 inside each group of 64, each group's scale, then the stage over bit 6.
-__global__ void __launch_bounds__(256, 3) int4_to_bf16_kernel(const __grid_constant__ Read4Launch a, int units) {
+// A warp takes `per` heads (of K's, then V's) of one tile in turn, the next one's codes on their way meanwhile.
+__global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_constant__ Read4Launch a, int units, int per) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, r = lane >> 2, tq = lane & 3, b = blockIdx.y;
-  const int unit = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int unit = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (unit >= units) return;
-  const int head = unit % (2 * a.Hkv), tile = unit / (2 * a.Hkv);
-  const bool is_v = head >= a.Hkv;
-  const int h = is_v ? head - a.Hkv : head;
+  const int groups = (2 * a.Hkv + per - 1) / per, tile = unit / groups;
+  const int first = (unit - tile * groups) * per, last = min(first + per, 2 * a.Hkv);
   const int p0 = a.pos[b], n = a.count[b];
   if (n <= 0) return;
   if (n > a.max_count) {
@@ -432,17 +453,33 @@ __global__ void __launch_bounds__(256, 3) int4_to_bf16_kernel(const __grid_const
   if (hi <= lo || base >= limit) return;
   const int from = page_of(a.from, b, T >> 2, a.err, lane == 0), to = page_of(a.to, b, T >> 2, a.err, lane == 0);
   if (from < 0 || to < 0) return;
-  const uint8_t* blk = a.pages4 + ((size_t)from * a.Hkv + h) * kBlock4Bytes + (size_t)(T & 3) * kTile4Bytes;
-  const uint8_t* cb = blk + (is_v ? kTile4V : 0) + 16 * lane;
-  const uint4 w0 = *reinterpret_cast<const uint4*>(cb), w1 = *reinterpret_cast<const uint4*>(cb + 512);
-  const uint8_t* sb = blk + kTile4Scales + (is_v ? 64 : 0);
+  const uint8_t* page = a.pages4 + (size_t)from * a.Hkv * kBlock4Bytes + (size_t)(T & 3) * kTile4Bytes;
+  uint4 c0, c1;     // the next head's codes,
+  uint32_t cs[2];   // and its scales of rows r, r + 8
+  auto load = [&](int head) {
+    const bool is_v = head >= a.Hkv;
+    const uint8_t* blk = page + (size_t)(is_v ? head - a.Hkv : head) * kBlock4Bytes;
+    const uint8_t* cb = blk + (is_v ? kTile4V : 0) + 16 * lane;
+    c0 = *reinterpret_cast<const uint4*>(cb);
+    c1 = *reinterpret_cast<const uint4*>(cb + 512);
+    const uint8_t* sb = blk + kTile4Scales + (is_v ? 64 : 0) + 4 * r;
+    cs[0] = *reinterpret_cast<const uint32_t*>(sb);
+    cs[1] = *reinterpret_cast<const uint32_t*>(sb + 32);
+  };
+  load(first);
+#pragma unroll 1
+  for (int head = first; head < last; ++head) {
+  const bool is_v = head >= a.Hkv;
+  const int h = is_v ? head - a.Hkv : head;
+  const uint4 w0 = c0, w1 = c1;
   float2 sc[2];
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
-    sc[rh] = __half22float2(*reinterpret_cast<const __half2*>(sb + 4 * (r + 8 * rh)));
+    sc[rh] = __half22float2(*reinterpret_cast<const __half2*>(&cs[rh]));
     sc[rh].x *= kInvSqrt128;
     sc[rh].y *= kInvSqrt128;
   }
+  if (head + 1 < last) load(head + 1);
   float2 d[8][4];  // [2 M + b2][2 nt + rh]
   // B[k][n] with n bits = channel bits 0, 3, 4 and nt = bit 1; k bits = bits 0, 3, 4, 1 (K) or 0, 1, 3, 4 (V)
   const int e0 = is_v ? ((tq >> 1) & (r >> 1)) & 1 : odd_bits(2 * tq & r);
@@ -503,6 +540,7 @@ __global__ void __launch_bounds__(256, 3) int4_to_bf16_kernel(const __grid_const
         reinterpret_cast<uint4*>(dst + (size_t)u * kD)[tq + 4 * M] = y;
       }
   }
+  }
 }
 
 int turn_of(const RopeLaunch& a) { return a.rotary == 0 ? kTurnNone : a.interleaved ? kTurnPairs : kTurnHalves; }
@@ -513,6 +551,15 @@ int split_of(const RopeLaunch& a, int rows) {
   int split = 1;
   while (split < 32 && 2 * split <= rows && (long long)a.tok.n_tokens * split < 256ll * a.num_sms) split *= 2;
   return split;
+}
+
+// Heads of a tile that a warp takes in turn, the next one's loads under the work on one: as many, up to eight, as
+// leave a group for each of the 16 warps that an SM holds (131,072 tokens of 8 heads in and out: 385 us with one head
+// a warp, 298 with two, 274 with four, 268 with eight; one request of 64 tokens has no such choice).
+int heads_of(long long tiles, int num_sms) {
+  int per = 1;
+  while (per < 8 && tiles >= 2 * per * 16ll * num_sms) per *= 2;
+  return per;
 }
 
 }  // namespace
@@ -537,7 +584,9 @@ cudaError_t launch_rope_append_bf16(const RopeLaunch& a, cudaStream_t stream) {
 
 cudaError_t launch_rope_append_int4(const RopeLaunch& a, cudaStream_t stream) {
   const int split = a.Hq ? split_of(a, a.Hq) : 1;
-  const long long units = ((long long)a.tok.max_tokens + 2 * kTile4 - 2) / kTile4 * 2 * a.Hkv;
+  const long long tiles = ((long long)a.tok.max_tokens + 2 * kTile4 - 2) / kTile4;
+  const int per = heads_of(tiles * a.pages.batch * 2 * a.Hkv, a.num_sms);
+  const long long units = tiles * ((2 * a.Hkv + per - 1) / per);
   const long long kv = (units + 3) / 4, qb = a.Hq ? ((long long)a.tok.max_tokens * split + 15) / 16 : 0;
   if (kv + qb > INT32_MAX || units > INT32_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(kv + qb), a.pages.batch);
@@ -545,19 +594,21 @@ cudaError_t launch_rope_append_int4(const RopeLaunch& a, cudaStream_t stream) {
                        reinterpret_cast<const void*>(rope_append_int4_kernel<kTurnHalves>),
                        reinterpret_cast<const void*>(rope_append_int4_kernel<kTurnPairs>)};
   RopeLaunch la = a;
-  int kv_blocks = (int)kv, n_units = (int)units, sp = split;
-  void* args[] = {&la, &kv_blocks, &n_units, &sp};
-  return launch_pdl(fn[turn_of(a)], grid, dim3(128), 0, stream, args);
+  int kv_blocks = (int)kv, n_units = (int)units, pr = per, sp = split;
+  void* args[] = {&la, &kv_blocks, &n_units, &pr, &sp};
+  return launch_pdl(fn[turn_of(a)], grid, dim3(128), 4 * 8192, stream, args);
 }
 
 cudaError_t launch_int4_to_bf16(const Read4Launch& a, cudaStream_t stream) {
-  const long long units = ((long long)a.max_count + 2 * kTile4 - 2) / kTile4 * 2 * a.Hkv;
+  const long long tiles = ((long long)a.max_count + 2 * kTile4 - 2) / kTile4;
+  int per = heads_of(tiles * a.from.batch * 2 * a.Hkv, a.num_sms);
+  const long long units = tiles * ((2 * a.Hkv + per - 1) / per);
   if (units > INT32_MAX - 8) return cudaErrorInvalidValue;
   Read4Launch la = a;
   int n_units = (int)units;
-  void* args[] = {&la, &n_units};
-  return launch_pdl(reinterpret_cast<const void*>(int4_to_bf16_kernel), dim3((unsigned)((units + 7) / 8), a.from.batch),
-                    dim3(256), 0, stream, args);
+  void* args[] = {&la, &n_units, &per};
+  return launch_pdl(reinterpret_cast<const void*>(int4_to_bf16_kernel), dim3((unsigned)((units + 3) / 4), a.from.batch),
+                    dim3(128), 0, stream, args);
 }
 
 }  // namespace oscar

@@ -48,20 +48,6 @@ constexpr int kWidePairs = 32;  // (query, KV head) pairs from which on the bloc
 constexpr int kSlack = 8;
 constexpr int kMaxRows = 1024;  // query rows whose lengths a block adds up; with more, a block takes one whole pair
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  const unsigned n = real ? 16u : 0u;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool real) {
-  const unsigned n = real ? 8u : 0u;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3, uint32_t p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
@@ -73,11 +59,6 @@ __device__ __forceinline__ void ldmatrix_x4_at(uint32_t& r0, uint32_t& r1, uint3
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                : "r"(p)
                : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
-  return v;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t p) {
   uint32_t v;
