@@ -227,6 +227,7 @@ __device__ __forceinline__ float max4(float m, float2 a, float2 b) {
 
 // A warp's `per` heads (of K's, then V's) of one tile: the next head's rows are on their way while one is turned and
 // rounded.  `sm`: 8 KB of the warp's own, two heads' rows, each lane's 16-byte pieces read by that lane alone.
+constexpr int kAhead4 = 2;  // heads of a warp in shared memory
 template <int TURN>
 __device__ __forceinline__ void append_tiles4(const RopeLaunch& a, int unit, int b, int per, uint32_t sm) {
   const int lane = threadIdx.x & 31, r = lane >> 2, tq = lane & 3;
@@ -255,25 +256,28 @@ __device__ __forceinline__ void append_tiles4(const RopeLaunch& a, int unit, int
     const uint16_t* x = (is_v ? a.v + (size_t)(head - a.Hkv) * kD : a.k + (size_t)head * kD) + 8 * tq;
     const uint16_t* x0 = v0 ? x + tok * stride : x;
     const uint16_t* x1 = v1 ? x + (tok + 8) * stride : x;
-    const uint32_t dst = sm + 4096 * (head & 1);
+    const uint32_t dst = sm + 4096 * (head % kAhead4);
 #pragma unroll
     for (int M = 0; M < 4; ++M) {
       cp_async16(dst + 512 * M, x0 + 32 * M, v0);
       cp_async16(dst + 512 * (4 + M), x1 + 32 * M, v1);
     }
   };
-  load(first);
-  cp_async_commit();
+#pragma unroll
+  for (int i = 0; i < kAhead4 - 1; ++i) {
+    if (first + i < last) load(first + i);
+    cp_async_commit();
+  }
 #pragma unroll 1
   for (int head = first; head < last; ++head) {
-  if (head + 1 < last) load(head + 1);
+  if (head + kAhead4 - 1 < last) load(head + kAhead4 - 1);
   cp_async_commit();
-  cp_async_wait<1>();
+  cp_async_wait<kAhead4 - 1>();
   const bool is_v = head >= a.Hkv;
   const int h = is_v ? head - a.Hkv : head;
   Tile4 t;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t.x[i >> 2][i & 3] = lds128(sm + 4096 * (head & 1) + 512 * i);
+  for (int i = 0; i < 8; ++i) t.x[i >> 2][i & 3] = lds128(sm + 4096 * (head % kAhead4) + 512 * i);
   if constexpr (TURN != kTurnNone)
     if (!is_v) turn_tile<TURN>(t, a, (int)base + r, v0, v1, tq);
   uint8_t* blk = a.pages4 + ((size_t)phys * a.Hkv + h) * kBlock4Bytes + (size_t)(T & 3) * kTile4Bytes;
@@ -407,7 +411,7 @@ __global__ void __launch_bounds__(128, 4) rope_append_int4_kernel(const __grid_c
     return;
   }
   const int warp = threadIdx.x >> 5, unit = blockIdx.x * 4 + warp;
-  if (unit < units) append_tiles4<TURN>(a, unit, blockIdx.y, per, smem_u32(sm) + 8192 * warp);
+  if (unit < units) append_tiles4<TURN>(a, unit, blockIdx.y, per, smem_u32(sm) + kAhead4 * 4096 * warp);
 }
 
 // ---------------------------------------------------------------- reading the 4-bit cache back
@@ -429,7 +433,8 @@ __device__ __forceinline__ uint32_t signs_f16(int lo, int hi) {
 
 // The transform back: the levels of 16 tokens as the MMA's rows (exact in fp16), the stages over bits
 // 2 and 5 inside each group of 64, each group's scale, then the stage over bit 6.
-// A warp takes `per` heads (of K's, then V's) of one tile in turn, the next one's codes on their way meanwhile.
+// A warp takes `per` heads (of K's, then V's) of one tile in turn, the codes of the next ones on their way meanwhile.
+constexpr int kAheadRead = 4;
 __global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_constant__ Read4Launch a, int units, int per) {
   griddep_launch_dependents();
   griddep_wait();
@@ -454,32 +459,40 @@ __global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_const
   const int from = page_of(a.from, b, T >> 2, a.err, lane == 0), to = page_of(a.to, b, T >> 2, a.err, lane == 0);
   if (from < 0 || to < 0) return;
   const uint8_t* page = a.pages4 + (size_t)from * a.Hkv * kBlock4Bytes + (size_t)(T & 3) * kTile4Bytes;
-  uint4 c0, c1;     // the next head's codes,
-  uint32_t cs[2];   // and its scales of rows r, r + 8
+  extern __shared__ __align__(16) uint8_t sm[];  // the heads ahead: [warp][kAheadRead] codes, scales
+  const uint32_t ring = smem_u32(sm) + (threadIdx.x >> 5) * (kAheadRead * 1088);
   auto load = [&](int head) {
-    const bool is_v = head >= a.Hkv;
-    const uint8_t* blk = page + (size_t)(is_v ? head - a.Hkv : head) * kBlock4Bytes;
-    const uint8_t* cb = blk + (is_v ? kTile4V : 0) + 16 * lane;
-    c0 = *reinterpret_cast<const uint4*>(cb);
-    c1 = *reinterpret_cast<const uint4*>(cb + 512);
-    const uint8_t* sb = blk + kTile4Scales + (is_v ? 64 : 0) + 4 * r;
-    cs[0] = *reinterpret_cast<const uint32_t*>(sb);
-    cs[1] = *reinterpret_cast<const uint32_t*>(sb + 32);
+    if (head < last) {
+      const bool is_v = head >= a.Hkv;
+      const uint8_t* blk = page + (size_t)(is_v ? head - a.Hkv : head) * kBlock4Bytes;
+      const uint8_t* cb = blk + (is_v ? kTile4V : 0) + 16 * lane;
+      const uint32_t dst = ring + 1088 * (head % kAheadRead) + 16 * lane;
+      cp_async16(dst, cb, true);
+      cp_async16(dst + 512, cb + 512, true);
+      if (lane < 4) cp_async16(dst + 1024, blk + kTile4Scales + (is_v ? 64 : 0) + 16 * lane, true);
+    }
+    cp_async_commit();
   };
-  load(first);
+#pragma unroll
+  for (int i = 0; i < kAheadRead - 1; ++i) load(first + i);
 #pragma unroll 1
   for (int head = first; head < last; ++head) {
   const bool is_v = head >= a.Hkv;
   const int h = is_v ? head - a.Hkv : head;
-  const uint4 w0 = c0, w1 = c1;
+  __syncwarp();
+  load(head + kAheadRead - 1);
+  cp_async_wait<kAheadRead - 1>();
+  __syncwarp();
+  const uint32_t stage = ring + 1088 * (head % kAheadRead);
+  const uint4 w0 = lds128(stage + 16 * lane), w1 = lds128(stage + 512 + 16 * lane);
   float2 sc[2];
 #pragma unroll
   for (int rh = 0; rh < 2; ++rh) {
-    sc[rh] = __half22float2(*reinterpret_cast<const __half2*>(&cs[rh]));
+    const uint32_t u = lds32(stage + 1024 + 4 * (r + 8 * rh));
+    sc[rh] = __half22float2(*reinterpret_cast<const __half2*>(&u));
     sc[rh].x *= kInvSqrt128;
     sc[rh].y *= kInvSqrt128;
   }
-  if (head + 1 < last) load(head + 1);
   float2 d[8][4];  // [2 M + b2][2 nt + rh]
   // B[k][n] with n bits = channel bits 0, 3, 4 and nt = bit 1; k bits = bits 0, 3, 4, 1 (K) or 0, 1, 3, 4 (V)
   const int e0 = is_v ? ((tq >> 1) & (r >> 1)) & 1 : odd_bits(2 * tq & r);
@@ -554,8 +567,8 @@ int split_of(const RopeLaunch& a, int rows) {
 }
 
 // Heads of a tile that a warp takes in turn, the next one's loads under the work on one: as many, up to eight, as
-// leave a group for each of the 16 warps that an SM holds (131,072 tokens of 8 heads in and out: 385 us with one head
-// a warp, 298 with two, 274 with four, 268 with eight; one request of 64 tokens has no such choice).
+// leave a group for each of the 16 warps that an SM holds (131,072 tokens of 8 heads in and out, with one head ahead:
+// 385 us with one head a warp, 298 with two, 274 with four, 268 with eight; a short call needs every warp).
 int heads_of(long long tiles, int num_sms) {
   int per = 1;
   while (per < 8 && tiles >= 2 * per * 16ll * num_sms) per *= 2;
@@ -596,7 +609,7 @@ cudaError_t launch_rope_append_int4(const RopeLaunch& a, cudaStream_t stream) {
   RopeLaunch la = a;
   int kv_blocks = (int)kv, n_units = (int)units, pr = per, sp = split;
   void* args[] = {&la, &kv_blocks, &n_units, &pr, &sp};
-  return launch_pdl(fn[turn_of(a)], grid, dim3(128), 4 * 8192, stream, args);
+  return launch_pdl(fn[turn_of(a)], grid, dim3(128), 4 * kAhead4 * 4096, stream, args);
 }
 
 cudaError_t launch_int4_to_bf16(const Read4Launch& a, cudaStream_t stream) {
@@ -608,7 +621,7 @@ cudaError_t launch_int4_to_bf16(const Read4Launch& a, cudaStream_t stream) {
   int n_units = (int)units;
   void* args[] = {&la, &n_units, &per};
   return launch_pdl(reinterpret_cast<const void*>(int4_to_bf16_kernel), dim3((unsigned)((units + 3) / 4), a.from.batch),
-                    dim3(128), 0, stream, args);
+                    dim3(128), 4 * kAheadRead * 1088, stream, args);
 }
 
 }  // namespace oscar

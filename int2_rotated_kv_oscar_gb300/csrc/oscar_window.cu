@@ -60,12 +60,6 @@ __device__ __forceinline__ void ldmatrix_x4_at(uint32_t& r0, uint32_t& r1, uint3
                : "r"(p)
                : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t p) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(p) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
