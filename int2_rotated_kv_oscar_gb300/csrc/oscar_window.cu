@@ -162,11 +162,12 @@ struct State {
 
 // 4-bit words to pairs of 16-bit floats, from the bits alone: a nibble in the mantissa under a fixed exponent.
 // K (fp16): the word two bits up and six down has its pairs at bits 2 and 6, where they read 256 + c and
-// 16 + c: two shifts and four LOP3 a word.  V (bf16, for the range of the weights): every pair at bit 3, 16 + c:
-// P V cancels the offset against the sum of the weights over all keys, and the MMA's fp32 sums truncate
-// relative to it, so it is kept small (the logits' offset is cancelled inside one tile's product).  The
-// exponent bits come in a register, so that masking and setting them is one LOP3 (as two constants they were two:
-// 64 of 370 instructions a tile).
+// 16 + c: two shifts and four LOP3 a word; the exponent bits come in a register, so that masking and setting them
+// is one LOP3 (as two constants they were two: 64 of 370 instructions a tile).  V (bf16, for the range of the
+// weights): the low byte of a bf16 without any more bits is a number n 2^-133 (subnormal, or its first binade), so a
+// nibble there reads c or 16 c of those, with one shift and four LOP3 a word, and the weights are 2^64 times larger.
+// P V has no offset but the levels' own 7.5, which it cancels against the sum of the weights over all keys: the
+// MMA's fp32 sums truncate relative to it.
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
   uint32_t y;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
@@ -181,8 +182,10 @@ __device__ __forceinline__ void k_pairs(uint32_t w, int b2, const KBits& k, uint
   lo = and_or(x, 0x003C003Cu, k.b256);
   hi = and_or(x, 0x03C003C0u, k.b16);
 }
-__device__ __forceinline__ uint32_t v_pair(uint32_t w, int i, uint32_t bits) {
-  return and_or(i == 0 ? w << 3 : w >> (4 * i - 3), 0x00780078u, bits);
+// pairs (2 h, 2 h + 1) of a word, x = w >> 8 h
+__device__ __forceinline__ void v_pairs(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  lo = x & 0x000F000Fu;
+  hi = x & 0x00F000F0u;
 }
 // D = A B + C, m16n8k16, fp16 operands, fp32 sums
 __device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -197,7 +200,8 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
   asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-constexpr float kKOffset0 = 256.f + 7.5f, kKOffset1 = 16.f + 7.5f, kVOffset = 16.f + 7.5f;
+constexpr float kKOffset0 = 256.f + 7.5f, kKOffset1 = 16.f + 7.5f, kVOffset = 7.5f;
+constexpr float kVUp = 18446744073709551616.f, kVDown = 590295810358705651712.f;  // 2^64; 2^69 = 2^133 / 2^64
 
 // value + residual of x as a bf16 pair (value in the low half)
 __device__ __forceinline__ uint32_t split_bf16(float x) {
@@ -454,7 +458,6 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     for (int e = 0; e < 4; ++e) st.o[i][e] = 0.f;
 
   const KBits kbits = {opaque(0x5C005C00u), opaque(0x4C004C00u)};
-  const uint32_t vbits = opaque(0x41804180u);
   // units of which the query sees all: [in0, in1) of the window
   const int in0 = (s.low + 15) >> 4, in1 = s.len >> 4;
   const int mine = u1 - u0 - warp > 0 ? (u1 - u0 - warp + kW - 1) / kW : 0;
@@ -579,6 +582,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         if constexpr (INT4) {
           const uint32_t u = lds32(stage + k * kTile4Bytes + kTile4Scales + 64 + 4 * (r + 8 * rh));
           float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&u));
+#pragma unroll
+          for (int e = 0; e < kH; ++e) p[e] *= kVUp;
           if ((hid >> (2 * k + rh)) & 1u) sc = make_float2(0.f, 0.f);  // a row nobody wrote may hold any scale
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
@@ -607,8 +612,10 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t wq = word_of(w, q);
-            mma_bf16_acc(st.o[4 * gr + q], v_pair(wq, 0, vbits), v_pair(wq, 1, vbits), v_pair(wq, 2, vbits),
-                         v_pair(wq, 3, vbits), bv[gr][0], bv[gr][1]);
+            uint32_t a0, a1, a2, a3;
+            v_pairs(wq, a0, a1);
+            v_pairs(wq >> 8, a2, a3);
+            mma_bf16_acc(st.o[4 * gr + q], a0, a1, a2, a3, bv[gr][0], bv[gr][1]);
           }
         }
       } else {
@@ -652,13 +659,14 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
                           : 16 * mt + 8 * hf + r;
       if constexpr (PACK) {
         float y = st.o[mt][2 * hf] + st.o[mt][2 * hf + 1];
-        if constexpr (INT4) y = fmaf(-kVOffset, st.wsum[0][mt >> 2], y);
+        if constexpr (INT4) y = fmaf(-kVOffset / kVUp, st.wsum[0][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
         if (tq < g) so[(warp * g + tq) * kD + ch] = y;
       } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y = st.o[mt][2 * hf + e];
-          if constexpr (INT4) y = fmaf(-kVOffset, st.wsum[e * (kH - 1)][mt >> 2], y);
+          if constexpr (INT4)
+            y = fmaf(-kVOffset / kVUp, st.wsum[e * (kH - 1)][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
           if (2 * tq + e < g) so[(warp * g + 2 * tq + e) * kD + ch] = y;
         }
       }
