@@ -160,30 +160,15 @@ struct State {
   float o[8][4];
 };
 
-// 4-bit words to pairs of 16-bit floats, from the bits alone: a nibble in the mantissa under a fixed exponent.
-// K (fp16): the word two bits up and six down has its pairs at bits 2 and 6, where they read 256 + c and
-// 16 + c: two shifts and four LOP3 a word; the exponent bits come in a register, so that masking and setting them
-// is one LOP3 (as two constants they were two: 64 of 370 instructions a tile).  V (bf16, for the range of the
-// weights): the low byte of a bf16 without any more bits is a number n 2^-133 (subnormal, or its first binade), so a
-// nibble there reads c or 16 c of those, with one shift and four LOP3 a word, and the weights are 2^64 times larger.
-// P V has no offset but the levels' own 7.5, which it cancels against the sum of the weights over all keys: the
-// MMA's fp32 sums truncate relative to it.
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
-  return y;
-}
-struct KBits {
-  uint32_t b256, b16;
-};
-// pairs (2 b2, 2 b2 + 1) of a word: channel bit 1 = 0 as 256 + c, = 1 as 16 + c
-__device__ __forceinline__ void k_pairs(uint32_t w, int b2, const KBits& k, uint32_t& lo, uint32_t& hi) {
-  const uint32_t x = b2 == 0 ? w << 2 : w >> 6;
-  lo = and_or(x, 0x003C003Cu, k.b256);
-  hi = and_or(x, 0x03C003C0u, k.b16);
-}
-// pairs (2 h, 2 h + 1) of a word, x = w >> 8 h
-__device__ __forceinline__ void v_pairs(uint32_t x, uint32_t& lo, uint32_t& hi) {
+// 4-bit words to pairs of 16-bit floats: the low byte of one without any exponent bits is a whole number of its
+// smallest subnormals (fp16: 2^-24, bf16: 2^-133, whose first binade goes on where they end), so a nibble in place reads
+// c or 16 c of those: one shift and four ANDs a word (with exponent bits over shifted nibbles: six shifts more for a
+// word of each, and offsets of 16 to 256 to cancel; 8 ragged requests 139 us).  K's queries are fp16 with a power of
+// two that makes up for it (and 16 times smaller where the codes are larger); V's weights are bf16, for their range,
+// and 2^64 times larger.  What is left is the levels' own 7.5: inside a tile's product for the logits, for P V against
+// the sum of the weights over all keys.
+// pairs (2 h, 2 h + 1) of a word, x = w >> 8 h, as c and 16 c
+__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t& lo, uint32_t& hi) {
   lo = x & 0x000F000Fu;
   hi = x & 0x00F000F0u;
 }
@@ -195,12 +180,8 @@ __device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-__device__ __forceinline__ uint32_t opaque(uint32_t x) {
-  uint32_t y;
-  asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-constexpr float kKOffset0 = 256.f + 7.5f, kKOffset1 = 16.f + 7.5f, kVOffset = 7.5f;
+constexpr float kOffset4 = 7.5f;
+constexpr float kKUnit = 5.9604644775390625e-8f;  // 2^-24
 constexpr float kVUp = 18446744073709551616.f, kVDown = 590295810358705651712.f;  // 2^64; 2^69 = 2^133 / 2^64
 
 // value + residual of x as a bf16 pair (value in the low half)
@@ -396,7 +377,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     butterfly(d, 1);
     butterfly(d, 2);
     butterfly(d, 4);
-    // fp16 with a power of two taken out (the largest channel becomes 8..16); PACK: value and residual (2^-22),
+    // fp16 with a power of two taken out (the largest channel becomes 2^14..2^15); PACK: value and residual (2^-22),
     // else the value alone (2^-11 of a channel's part of the logit)
     float top = 0.f;
 #pragma unroll
@@ -405,19 +386,19 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
       for (int nt = 0; nt < 2; ++nt) top = fmaxf(top, fmaxf(fabsf(d[i][nt].x), fabsf(d[i][nt].y)));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // 2^(3 - floor(log2 top)) and its inverse, from the exponent bits (kept where both are normal)
-    const int ex = min(max((int)(__float_as_uint(top) >> 23), 8), 250);
-    const float up = __uint_as_float((uint32_t)(127 + 3 - (ex - 127)) << 23), down = __uint_as_float((uint32_t)(ex - 3) << 23);
+    // 2^(14 - floor(log2 top)) and its inverse times 2^24, from the exponent bits (kept where both are normal)
+    const int ex = min(max((int)(__float_as_uint(top) >> 23), 15), 244);
+    const float up = __uint_as_float((uint32_t)(127 + 14 - (ex - 127)) << 23), down = __uint_as_float((uint32_t)(ex + 10) << 23);
     float part[2] = {0.f, 0.f};
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
       for (int kh = 0; kh < 2; ++kh) {
-        const float x0 = d[ks][kh].x * up, x1 = d[ks][kh].y * up;
+        const float x0 = d[ks][kh].x * (kh ? up / 16.f : up), x1 = d[ks][kh].y * (kh ? up / 16.f : up);
         __half2 v = __floats2half2_rn(x0, x1);
         if (PACK && (r & 1)) v = __floats2half2_rn(x0 - __low2float(v), x1 - __high2float(v));
         qf[ks][kh] = h2_as_u32(v);
-        part[ks >> 2] = fmaf(kh ? -kKOffset1 : -kKOffset0, __low2float(v) + __high2float(v), part[ks >> 2]);
+        part[ks >> 2] = fmaf(kh ? -16.f * kOffset4 * kKUnit : -kOffset4 * kKUnit, __low2float(v) + __high2float(v), part[ks >> 2]);
       }
     // sums over the column's four lanes, then to the lanes that hold columns 2 tq, 2 tq + 1 of the logits
 #pragma unroll
@@ -457,7 +438,6 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) st.o[i][e] = 0.f;
 
-  const KBits kbits = {opaque(0x5C005C00u), opaque(0x4C004C00u)};
   // units of which the query sees all: [in0, in1) of the window
   const int in0 = (s.low + 15) >> 4, in1 = s.len >> 4;
   const int mine = u1 - u0 - warp > 0 ? (u1 - u0 - warp + kW - 1) / kW : 0;
@@ -482,8 +462,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           uint32_t a0, a1, a2, a3;
-          k_pairs(word_of(w0, ks >> 1), ks & 1, kbits, a0, a2);
-          k_pairs(word_of(w1, ks >> 1), ks & 1, kbits, a1, a3);
+          code_pairs(word_of(w0, ks >> 1) >> (8 * (ks & 1)), a0, a2);
+          code_pairs(word_of(w1, ks >> 1) >> (8 * (ks & 1)), a1, a3);
           if ((ks & 3) == 0)  // the group's sum starts from the offset's part
             mma_f16_from(acc[ks >> 2], a0, a1, a2, a3, qf[ks][0], qf[ks][1], q0[ks >> 2]);
           else
@@ -613,8 +593,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
           for (int q = 0; q < 4; ++q) {
             const uint32_t wq = word_of(w, q);
             uint32_t a0, a1, a2, a3;
-            v_pairs(wq, a0, a1);
-            v_pairs(wq >> 8, a2, a3);
+            code_pairs(wq, a0, a1);
+            code_pairs(wq >> 8, a2, a3);
             mma_bf16_acc(st.o[4 * gr + q], a0, a1, a2, a3, bv[gr][0], bv[gr][1]);
           }
         }
@@ -659,14 +639,14 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
                           : 16 * mt + 8 * hf + r;
       if constexpr (PACK) {
         float y = st.o[mt][2 * hf] + st.o[mt][2 * hf + 1];
-        if constexpr (INT4) y = fmaf(-kVOffset / kVUp, st.wsum[0][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
+        if constexpr (INT4) y = fmaf(-kOffset4 / kVUp, st.wsum[0][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
         if (tq < g) so[(warp * g + tq) * kD + ch] = y;
       } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y = st.o[mt][2 * hf + e];
           if constexpr (INT4)
-            y = fmaf(-kVOffset / kVUp, st.wsum[e * (kH - 1)][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
+            y = fmaf(-kOffset4 / kVUp, st.wsum[e * (kH - 1)][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
           if (2 * tq + e < g) so[(warp * g + 2 * tq + e) * kD + ch] = y;
         }
       }
