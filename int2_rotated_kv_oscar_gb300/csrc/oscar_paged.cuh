@@ -61,6 +61,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t p) {
   return v;
 }
 
+// The codes of a 4-bit word as 16-bit floats without exponent bits, whole numbers of their smallest subnormals
+// (fp16: 2^-24; bf16: 2^-133, on into the first binade): pairs (2 h, 2 h + 1) of a word, x = w >> 8 h, as c and 16 c
+__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  lo = x & 0x000F000Fu;
+  hi = x & 0x00F000F0u;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 

@@ -415,24 +415,19 @@ __global__ void __launch_bounds__(128, 4) rope_append_int4_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- reading the 4-bit cache back
-// Four pairs of levels c - 7.5 of a word as fp16: pair i = nibbles (i, i + 4).
-// 1024 + 16 c comes from the bits alone (0x6400 | c << 4); times 1/16, minus 71.5 is exact.
-__device__ __forceinline__ void levels4(uint32_t w, uint32_t (&v)[4]) {
-  const __half2 k = __half2half2(__ushort_as_half(0x2C00)), o = __half2half2(__ushort_as_half(0xD478));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t sh = i == 0 ? w << 4 : w >> (4 * (i - 1));
-    uint32_t x = (sh & 0x00F000F0u) | 0x64006400u;
-    v[i] = h2_as_u32(__hfma2(*reinterpret_cast<__half2*>(&x), k, o));
-  }
+// The codes of a word as fp16 numbers c 2^-24 (pairs 0, 2: nibbles i and i + 4) and 16 c 2^-24 (pairs 1, 3).
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t (&v)[4]) {
+  code_pairs(w, v[0], v[1]);
+  code_pairs(w >> 8, v[2], v[3]);
 }
 
 __device__ __forceinline__ uint32_t signs_f16(int lo, int hi) {
   return 0x3C003C00u ^ ((uint32_t)lo << 15) ^ ((uint32_t)hi << 31);
 }
 
-// The transform back: the levels of 16 tokens as the MMA's rows (exact in fp16), the stages over bits
-// 2 and 5 inside each group of 64, each group's scale, then the stage over bit 6.
+// The transform back: the codes of 16 tokens as the MMA's rows (the signs of the ones that are 16 times larger are
+// +-1/16; the levels' -7.5 add up to -7.5 x 16 in the column of ones alone, where the sum starts: all of it exact),
+// the stages over bits 2 and 5 inside each group of 64, each group's scale, then the stage over bit 6.
 // A warp takes `per` heads (of K's, then V's) of one tile in turn, the codes of the next ones on their way meanwhile.
 constexpr int kAheadRead = 4;
 __global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_constant__ Read4Launch a, int units, int per) {
@@ -490,8 +485,8 @@ __global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_const
   for (int rh = 0; rh < 2; ++rh) {
     const uint32_t u = lds32(stage + 1024 + 4 * (r + 8 * rh));
     sc[rh] = __half22float2(*reinterpret_cast<const __half2*>(&u));
-    sc[rh].x *= kInvSqrt128;
-    sc[rh].y *= kInvSqrt128;
+    sc[rh].x *= kInvSqrt128 * 16777216.f;
+    sc[rh].y *= kInvSqrt128 * 16777216.f;
   }
   float2 d[8][4];  // [2 M + b2][2 nt + rh]
   // B[k][n] with n bits = channel bits 0, 3, 4 and nt = bit 1; k bits = bits 0, 3, 4, 1 (K) or 0, 1, 3, 4 (V)
@@ -504,8 +499,8 @@ __global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_const
   if (!is_v) {
 #pragma unroll
     for (int M = 0; M < 4; ++M) {
-      levels4(word_of(w0, M), lev[0][M]);
-      levels4(word_of(w1, M), lev[1][M]);
+      codes4(word_of(w0, M), lev[0][M]);
+      codes4(word_of(w1, M), lev[1][M]);
     }
   }
 #pragma unroll
@@ -516,13 +511,14 @@ __global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_const
       a0 = lev[0][M][2 * b2], a1 = lev[1][M][2 * b2], a2 = lev[0][M][2 * b2 + 1], a3 = lev[1][M][2 * b2 + 1];
     } else {  // a word holds a 16-channel x 16-token block with the channels as rows: transpose its quarters
       uint32_t v[4];
-      levels4(i < 4 ? word_of(w0, i) : word_of(w1, i - 4), v);
+      codes4(i < 4 ? word_of(w0, i) : word_of(w1, i - 4), v);
       a0 = movmatrix_trans(v[0]), a1 = movmatrix_trans(v[2]), a2 = movmatrix_trans(v[1]), a3 = movmatrix_trans(v[3]);
     }
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(acc, a0, a1, a2, a3, nt ? s ^ nt_lo : s, (nt ? s ^ nt_hi : s) ^ flip_hi);
+      const float first = nt == 0 && tq == 0 ? -7.5f * 16.f / 16777216.f : 0.f;
+      float acc[4] = {first, 0.f, first, 0.f};
+      mma_f16(acc, a0, a1, a2, a3, nt ? s ^ nt_lo : s, ((nt ? s ^ nt_hi : s) ^ flip_hi) - 0x10001000u);
       d[i][2 * nt] = make_float2(acc[0], acc[1]);
       d[i][2 * nt + 1] = make_float2(acc[2], acc[3]);
     }

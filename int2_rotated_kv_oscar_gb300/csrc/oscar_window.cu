@@ -167,11 +167,6 @@ struct State {
 // two that makes up for it (and 16 times smaller where the codes are larger); V's weights are bf16, for their range,
 // and 2^64 times larger.  What is left is the levels' own 7.5: inside a tile's product for the logits, for P V against
 // the sum of the weights over all keys.
-// pairs (2 h, 2 h + 1) of a word, x = w >> 8 h, as c and 16 c
-__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  lo = x & 0x000F000Fu;
-  hi = x & 0x00F000F0u;
-}
 // D = A B + C, m16n8k16, fp16 operands, fp32 sums
 __device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1, const float (&c)[4]) {
