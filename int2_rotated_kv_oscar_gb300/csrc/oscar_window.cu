@@ -32,9 +32,9 @@ constexpr float kLog2eW = 1.4426950408889634f;
 constexpr float kLazyW = 8.0f;  // the accumulators are rescaled when the maximum grows by more than 2^8
 
 // WIDE: 16 warps and one block per SM (4 bits), for few pairs, whose cuts each cost a join (batch 1 x 100K, 8
-// pairs: 29.9 us, 33.3 us with two blocks of 8); else two blocks of 8, one of which copies and computes while the
-// other begins or joins a segment (28 requests x 4160 visible keys, 224 pairs: 39.4 us against 44.3; 8 ragged
-// requests, 64 pairs: 138 against 142).  BF16 has one block of 8 (its units are larger).
+// pairs: 27.5 us, 30.4 us with two blocks of 8); else two blocks of 8, one of which copies and computes while the
+// other begins or joins a segment (28 requests x 4160 visible keys, 224 pairs: 35.9 us against 41.7; 8 ragged
+// requests, 64 pairs: 126 against 131).  BF16 has one block of 8 (its units are larger).
 template <bool INT4, bool WIDE>
 struct Ring {
   static constexpr int kWarps = INT4 && WIDE ? 16 : 8;
