@@ -143,6 +143,9 @@ def int4_view(pages, page_table):
     """oscar_int4_cache_view of contiguous pages uint8 [num_pages, Hkv, 8704] and page_table int32 [batch, max_pages].
     The struct keeps the tensors alive for as long as it lives (it holds their addresses)."""
     _contiguous(pages, page_table)
+    _types((torch.uint8, pages), (torch.int32, page_table))
+    if pages.dim() != 3 or pages.shape[2] != abi.INT4_BLOCK_BYTES or page_table.dim() != 2:
+        raise ValueError("pages must be [num_pages, Hkv, %d], page_table [batch, max_pages]" % abi.INT4_BLOCK_BYTES)
     v = abi.oscar_int4_cache_view(pages=pages.data_ptr(), num_pages=pages.shape[0], page_table=page_table.data_ptr(),
                                   max_pages_per_req=page_table.shape[1], batch=page_table.shape[0])
     v._tensors = (pages, page_table)
@@ -152,6 +155,10 @@ def int4_view(pages, page_table):
 def bf16_view(k_pages, v_pages, page_table):
     """oscar_bf16_cache_view of contiguous pools bf16 [num_pages, Hkv, 64, 128] and page_table int32 [batch, max_pages]."""
     _contiguous(k_pages, v_pages, page_table)
+    _types((torch.bfloat16, k_pages, v_pages), (torch.int32, page_table))
+    if (k_pages.dim() != 4 or k_pages.shape[2:] != (abi.PAGE_TOKENS, abi.HEAD_DIM) or v_pages.shape != k_pages.shape
+            or page_table.dim() != 2):
+        raise ValueError("pools must be [num_pages, Hkv, 64, 128], page_table [batch, max_pages]")
     v = abi.oscar_bf16_cache_view(k_pages=k_pages.data_ptr(), v_pages=v_pages.data_ptr(), num_pages=k_pages.shape[0],
                                   page_table=page_table.data_ptr(), max_pages_per_req=page_table.shape[1],
                                   batch=page_table.shape[0])
@@ -161,7 +168,21 @@ def bf16_view(k_pages, v_pages, page_table):
 
 def _contiguous(*tensors):
     if not all(t.is_contiguous() for t in tensors):
-        raise ValueError("pools and page tables must be contiguous")
+        raise ValueError("only q, k, v and q_out may be parts of wider rows")
+
+
+def _types(*groups):
+    """Each group is a type and the tensors (or None) that must have it; all of them lie on one device."""
+    device = None
+    for dtype, *tensors in groups:
+        for t in tensors:
+            if t is None:
+                continue
+            if t.dtype != dtype:
+                raise ValueError("a tensor of type %s where %s belongs" % (t.dtype, dtype))
+            if device is not None and t.device != device:
+                raise ValueError("tensors on %s and %s" % (device, t.device))
+            device = t.device
 
 
 def _token_stride(x, name):
@@ -184,8 +205,11 @@ def rope_append_args(k, v, pos, q=None, q_out=None, rope=None, interleaved=False
     slices of a wider row) and a float32 rope table [n_positions, rotary_dim] (None: no rotation).
     The struct keeps the tensors alive."""
     n = int(k.shape[0])
-    if rope is not None:
-        _contiguous(rope)
+    _types((torch.bfloat16, k, v, q, q_out), (torch.float32, rope), (torch.int32, pos, cu_seqlens))
+    _contiguous(*(t for t in (rope, pos, cu_seqlens) if t is not None))
+    if v.shape != k.shape or (q is None) != (q_out is None) or (
+            q is not None and (q.shape[0] != n or q_out.shape != q.shape)) or (rope is not None and rope.dim() != 2):
+        raise ValueError("k and v, and q and q_out, must have one shape and n_tokens rows, rope two dimensions")
     a = abi.oscar_rope_append_args(
         q=None if q is None else q.data_ptr(), q_out=None if q_out is None else q_out.data_ptr(), k=k.data_ptr(),
         v=v.data_ptr(), q_stride=0 if q is None else _token_stride(q, "q"),
@@ -203,8 +227,11 @@ def window_args(q, out, pos, ctx_len, max_ctx_len, window=-1, sinks=0, cu_seqlen
                 sm_scale=0.0):
     """oscar_window_args for bf16 q [n_tokens, Hq, 128] (may be a slice of a wider row) and contiguous bf16 out.
     The struct keeps the tensors alive."""
-    _contiguous(out)
     n = int(q.shape[0])
+    _types((torch.bfloat16, q, out), (torch.int32, pos, ctx_len, cu_seqlens))
+    _contiguous(*(t for t in (out, pos, ctx_len, cu_seqlens) if t is not None))
+    if out.shape != q.shape:
+        raise ValueError("q and out must have one shape")
     a = abi.oscar_window_args(
         q=q.data_ptr(), out=out.data_ptr(), pos=pos.data_ptr(),
         cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr(), ctx_len=ctx_len.data_ptr(),

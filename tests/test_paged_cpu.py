@@ -43,3 +43,29 @@ def test_helpers_refuse_what_the_structs_cannot_say():
         kv.window_args(torch.zeros(3, 4, 130, dtype=torch.bfloat16)[:, :, :128], torch.zeros_like(q), i, i, 10)
     with pytest.raises(ValueError):  # a result with gaps
         kv.window_args(q, torch.zeros(3, 6, 128, dtype=torch.bfloat16)[:, 1:5], i, i, 10)
+    for bad in (q.float(), q[:2], q[:, :2]):  # another type, fewer rows, fewer heads than q
+        with pytest.raises(ValueError):
+            kv.window_args(q, bad.contiguous(), i, i, 10)
+    with pytest.raises(ValueError):
+        kv.window_args(q, torch.zeros_like(q), i.long(), i, 10)
+    with pytest.raises(ValueError):
+        kv.window_args(q, torch.zeros_like(q), torch.zeros(6, dtype=torch.int32)[::2], i, 10)
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    rope = torch.zeros(16, 128)
+    assert kv.rope_append_args(k, k.clone(), i, q=q, q_out=q, rope=rope).rotary_dim == 128
+    for change in (dict(v=k[:2]), dict(q=q), dict(q=q[:2], q_out=q[:2]), dict(q=q, q_out=q[:, :2]), dict(rope=rope.double()),
+                   dict(rope=rope[:, ::2]), dict(rope=rope[0]), dict(pos=i.long()), dict(cu_seqlens=i.long())):
+        a = dict(k=k, v=k.clone(), pos=i)
+        a.update(change)
+        with pytest.raises(ValueError):
+            kv.rope_append_args(**a)
+    table = torch.zeros(2, 4, dtype=torch.int32)
+    pool = torch.zeros(3, 2, 64, 128, dtype=torch.bfloat16)
+    codes = torch.zeros(3, 2, abi.INT4_BLOCK_BYTES, dtype=torch.uint8)
+    assert (kv.bf16_view(pool, pool.clone(), table).batch, kv.int4_view(codes, table).max_pages_per_req) == (2, 4)
+    for bad in ((pool, pool[:2], table), (pool.half(), pool.half(), table), (pool, pool, table.long()), (pool, pool, table[0])):
+        with pytest.raises(ValueError):
+            kv.bf16_view(*bad)
+    for bad in ((codes[:, :, :8192].contiguous(), table), (codes.char(), table), (codes, table.long()), (codes, table[:, ::2])):
+        with pytest.raises(ValueError):
+            kv.int4_view(*bad)
