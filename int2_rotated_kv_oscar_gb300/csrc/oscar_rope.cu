@@ -98,7 +98,8 @@ __device__ __forceinline__ void rope_rows(const RopeLaunch& a, int block, int b,
 
 template <int TURN>
 __global__ void __launch_bounds__(256) rope_append_bf16_kernel(const __grid_constant__ RopeLaunch a, int split) {
-  griddep_launch_dependents();
+  // (no early launch of what comes next: the mixed cache's append of a fresh prompt reads its K and V beside the kernel
+  // before it, and they may be this one's q_out)
   griddep_wait();
   rope_rows<TURN, true, 256>(a, blockIdx.x, blockIdx.y, split);
 }
@@ -408,8 +409,7 @@ template <int TURN>
 __global__ void __launch_bounds__(128, 4) rope_append_int4_kernel(const __grid_constant__ RopeLaunch a, int kv_blocks,
                                                                int units, int per, int split) {
   extern __shared__ __align__(16) uint8_t sm[];
-  griddep_launch_dependents();
-  griddep_wait();
+  griddep_wait();  // (and no early launch of what comes next, as above)
   if ((int)blockIdx.x >= kv_blocks) {  // the queries' rows
     rope_rows<TURN, false, 128>(a, blockIdx.x - kv_blocks, blockIdx.y, split);
     return;
@@ -436,8 +436,8 @@ __device__ __forceinline__ uint32_t signs_f16(int lo, int hi) {
 // (131,072 tokens x 8 heads of K and V: 107 us, 93% of the copy bandwidth; 82 us, 93%, at 100,000.)
 constexpr int kAheadRead = 4;
 __global__ void __launch_bounds__(128, 4) int4_to_bf16_kernel(const __grid_constant__ Read4Launch a, int units, int per) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31, r = lane >> 2, tq = lane & 3, b = blockIdx.y;
   const int unit = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (unit >= units) return;

@@ -197,8 +197,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   __shared__ int sm_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, tq = lane & 3;
   __shared__ int pre[kMaxRows + 1], scan[kW];
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();  // (behind the wait: what is before this kernel is complete once the next one starts)
   const int g = a.Hq / a.Hkv, rows = a.tok.n_tokens, G = gridDim.x, block = blockIdx.x;
   const bool few = rows <= 32;  // each warp adds the rows up for itself, lane i row i
   int at = 0, end = 1, total = 0;  // this block's range of all units

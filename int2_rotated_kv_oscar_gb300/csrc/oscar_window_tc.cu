@@ -400,7 +400,6 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_at + 2);
   // [0, 1] the relay of tile t gave up; [2] a page outside the pool was met
   int* words = reinterpret_cast<int*>(sm + kTcwBars + 192);     // [8] the pairs' words
-  griddep_launch_dependents();
   if (threadIdx.x < 8) words[threadIdx.x] = 0;
   if (threadIdx.x < 3) flags[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
@@ -427,6 +426,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
   __syncthreads();
   tc_fence_after();
   griddep_wait();
+  griddep_launch_dependents();
   bool gave_up = false;
   TcwItem it;
 
@@ -769,13 +769,13 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
 // now 18; 256 at 100,000 329 us, now 300.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_constant__ TcwArgs ta) {
-  griddep_launch_dependents();
   const WindowLaunch& a = ta.a;
   const int g = a.Hq / a.Hkv, lane = threadIdx.x & 31, i = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int q = i / g, head = i - q * g;  // the row's query among its tile pair's, and its query head
   int pair, h, p0, n, row0;
   const int b = ta.by_heads.divide(ta.by_tiles.divide((int)blockIdx.y, pair), h);
   griddep_wait();
+  griddep_launch_dependents();
   if (!token_span(a.tok, b, p0, n, row0, a.err, false) || q >= 2 * ta.qpt || pair * 2 * ta.qpt + q >= n) return;
   const int tt = q >= ta.qpt, r = (q - tt * ta.qpt) * g + head;
   const float c = a.sm_scale * kLog2eT;

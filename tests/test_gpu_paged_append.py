@@ -321,3 +321,35 @@ def test_append_refusals():
     with pytest.raises(ValueError):
         kv.rope_append_args(c.k[:, :, :64], c.v, c.pos)
     c.close()
+
+
+def test_rotated_rows_feed_the_mixed_cache_at_once():
+    """q_out as the K of the mixed cache's append of a fresh prompt, which copies BF16 rows beside the kernel before it."""
+    H, n = 2, 6000
+    ctx = context(H, H)
+    eye = np.eye(128, dtype=np.float32)
+    abi.oscar_load_rotation(ctx, 0, eye, eye, 1.0, 1.0)
+    mixed = kv.MixedCache(1, H, n // 64 + 2, 1, 1, 1, n // 64 + 2)
+    mixed.page_table.copy_(torch.arange(n // 64 + 2, device=DEV, dtype=torch.int32)[None])
+    rope = kv.rope_table(ctx, n)
+    k_pages, v_pages = nan_pages(n // 64 + 1, H)
+    view = kv.bf16_view(k_pages, v_pages, torch.arange(n // 64 + 1, device=DEV, dtype=torch.int32)[None])
+    pages = nan_int4(n // 64 + 1, H)
+    view4 = kv.int4_view(pages, torch.arange(n // 64 + 1, device=DEV, dtype=torch.int32)[None])
+    pos, cu = ints([0]), ints([0, n])
+    for i in range(6):
+        x = torch.randn(n, 2 * H, 128, generator=torch.Generator(DEV).manual_seed(i), device=DEV).to(torch.bfloat16)
+        turned = torch.full((n, H, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+        rows = kv.rope_append_args(x[:, :H], x[:, H:], pos, q=x[:, :H], q_out=turned, rope=rope, cu_seqlens=cu)
+        values = x[:, H:].contiguous()
+        torch.cuda.synchronize()
+        if i % 2:
+            abi.oscar_rope_append_int4(ctx, view4, rows)
+        else:
+            abi.oscar_rope_append_bf16(ctx, view, rows)
+        abi.oscar_kv_append(ctx, 0, mixed.view(0), kv.append_args(turned, values, pos, cu_seqlens=cu, fresh_ring=True))
+        assert abi.oscar_check_device_error(ctx) == 0
+        at = torch.arange(n - 256, n, device=DEV)
+        assert torch.equal(mixed.k_ring[0][0][:, (at - 64) % 256].transpose(0, 1), turned[at])
+        assert torch.equal(mixed.k_sink[0][0].transpose(0, 1), turned[:64])
+    abi.oscar_destroy(ctx)
