@@ -156,7 +156,10 @@ template <bool PACK, bool INT4>
 struct State {
   static constexpr int kH = PACK ? 1 : 2;
   float m[kH], l[kH];
-  float wsum[kH][2];  // 4-bit: sums of the weights of each group (what the codes' offset is multiplied by)
+  // 4-bit: sums of the weights of each group (what the levels' offset is multiplied by).  Two heads a lane: as the
+  // products of rows of ones, two MMAs a tile for sixteen instructions (8 ragged requests 126 -> 121 us); one head: in
+  // [g][0] this lane's part, whose two additions a row are cheaper than the registers (batch 1 x 100K 28.1 us with them)
+  float wsum[2][PACK ? 1 : 4];
   float o[8][4];
 };
 
@@ -326,6 +329,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   at += wa.cut ? u1 - u0 : 1;
   const uint32_t ring = smem_u32(sm) + warp * (kS * R::kUnit);
   int phys_l = -1, fetched = 0;  // lane i: the page of the warp's unit fetched - 32 + i
+  uint32_t put = ring;  // the next unit copied goes there
   auto issue = [&](int i) {      // the warp's i-th unit
     if (i >= fetched) {
       const int u = u0 + warp + (fetched + lane) * kW;
@@ -335,7 +339,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     }
     const int phys = __shfl_sync(0xffffffffu, phys_l, i & 31);
     const int u = u0 + warp + i * kW;
-    if (u < u1) copy_unit<INT4>(a, s, s.tile(u * KU), phys, h, ring + (i % kS) * R::kUnit, lane);
+    if (u < u1) copy_unit<INT4>(a, s, s.tile(u * KU), phys, h, put, lane);
+    put = put == ring + (kS - 1) * R::kUnit ? ring : put + R::kUnit;
     cp_async_commit();
     return phys;
   };
@@ -426,12 +431,15 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   for (int i = 0; i < kH; ++i) {
     st.m[i] = -INFINITY;
     st.l[i] = 0.f;
-    st.wsum[i][0] = st.wsum[i][1] = 0.f;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) st.o[i][e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < (PACK ? 1 : 4); ++e) st.wsum[i][e] = 0.f;
 
   // units of which the query sees all: [in0, in1) of the window
   const int in0 = (s.low + 15) >> 4, in1 = s.len >> 4;
@@ -441,7 +449,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     phys_q[kS - 1] = issue(i + kS - 1);
     cp_async_wait<kS - 1>();
     __syncwarp();
-    const uint32_t stage = ring + (i % kS) * R::kUnit;
+    const uint32_t stage = put;  // (kS - 1 units ahead of the one used now: the copy after next goes where that is)
     const int T = s.tile((u0 + warp + i * kW) * KU);
     const bool bad = phys_q[0] < 0;
 #pragma unroll
@@ -532,13 +540,16 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         f[e] = st.m[e] == -INFINITY ? 0.f : exp2_fast((st.m[e] - m) * qscale[e]);
         st.m[e] = m;
         st.l[e] *= f[e];
-        st.wsum[e][0] *= f[e];
-        st.wsum[e][1] *= f[e];
       }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) st.o[mt][e] *= PACK ? f[0] : f[(e & 1) * (kH - 1)];
+      if constexpr (INT4)
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+          for (int e = 0; e < (PACK ? 1 : 4); ++e) st.wsum[gr][e] *= PACK ? f[0] : f[(e & 1) * (kH - 1)];
     }
 #pragma unroll
     for (int e = 0; e < kH; ++e) sub[e] = st.m[e] == -INFINITY ? 0.f : -st.m[e] * qscale[e];
@@ -565,14 +576,11 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
             const float sg = gr ? sc.y : sc.x;
             if constexpr (PACK) {
               const float w = p[0] * sg;
-              st.wsum[0][gr] += w;
+              st.wsum[gr][0] += w;
               bv[gr][rh] = movmatrix_trans(split_bf16(w));
             } else {
               // one bf16 term per weight (2^-9): the offset is taken off with the rounded weights
-              const uint32_t w = pack_bf16x2(p[0] * sg, p[kH - 1] * sg);
-              st.wsum[0][gr] += bf16_lo(w);
-              st.wsum[kH - 1][gr] += bf16_hi(w);
-              bv[gr][rh] = movmatrix_trans(w);
+              bv[gr][rh] = movmatrix_trans(pack_bf16x2(p[0] * sg, p[kH - 1] * sg));
             }
           }
         } else {
@@ -584,6 +592,10 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr) {
           const uint4 w = lds128(vb + 512 * gr);
+          if constexpr (!PACK) {
+            constexpr uint32_t kOnes = 0x3F803F80u;
+            mma_bf16_acc(st.wsum[gr], kOnes, kOnes, kOnes, kOnes, bv[gr][0], bv[gr][1]);
+          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t wq = word_of(w, q);
@@ -609,12 +621,12 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
   for (int e = 0; e < kH; ++e)
 #pragma unroll
+    for (int o = 4; o < 32; o <<= 1) st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], o);
+  if constexpr (INT4 && PACK)
+#pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
-      st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], o);
-      if constexpr (INT4) {
-        st.wsum[e][0] += __shfl_xor_sync(0xffffffffu, st.wsum[e][0], o);
-        st.wsum[e][1] += __shfl_xor_sync(0xffffffffu, st.wsum[e][1], o);
-      }
+      st.wsum[0][0] += __shfl_xor_sync(0xffffffffu, st.wsum[0][0], o);
+      st.wsum[1][0] += __shfl_xor_sync(0xffffffffu, st.wsum[1][0], o);
     }
   __syncthreads();  // every warp is done with the ring: it becomes the warps' accumulators [warp][head][128]
   float* so = reinterpret_cast<float*>(sm);
@@ -634,14 +646,14 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
                           : 16 * mt + 8 * hf + r;
       if constexpr (PACK) {
         float y = st.o[mt][2 * hf] + st.o[mt][2 * hf + 1];
-        if constexpr (INT4) y = fmaf(-kOffset4 / kVUp, st.wsum[0][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
+        if constexpr (INT4) y = fmaf(-kOffset4 / kVUp, st.wsum[mt >> 2][0], y * (hf ? kVDown / 16.f : kVDown));
         if (tq < g) so[(warp * g + tq) * kD + ch] = y;
       } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y = st.o[mt][2 * hf + e];
           if constexpr (INT4)
-            y = fmaf(-kOffset4 / kVUp, st.wsum[e * (kH - 1)][mt >> 2], y * (hf ? kVDown / 16.f : kVDown));
+            y = fmaf(-kOffset4 / kVUp, st.wsum[mt >> 2][e], y * (hf ? kVDown / 16.f : kVDown));
           if (2 * tq + e < g) so[(warp * g + 2 * tq + e) * kD + ch] = y;
         }
       }
