@@ -163,13 +163,19 @@ struct State {
   float o[8][4];
 };
 
-// 4-bit words to pairs of 16-bit floats: the low byte of one without any exponent bits is a whole number of its
-// smallest subnormals (fp16: 2^-24, bf16: 2^-133, whose first binade goes on where they end), so a nibble in place reads
-// c or 16 c of those: one shift and four ANDs a word (with exponent bits over shifted nibbles: six shifts more for a
-// word of each, and offsets of 16 to 256 to cancel; 8 ragged requests 139 us).  K's queries are fp16 with a power of
-// two that makes up for it (and 16 times smaller where the codes are larger); V's weights are bf16, for their range,
-// and 2^64 times larger.  What is left is the levels' own 7.5: inside a tile's product for the logits, for P V against
-// the sum of the weights over all keys.
+// 4-bit words to operands: the low byte of a 16-bit float without any exponent bits is a whole number of its smallest
+// subnormals (fp16: 2^-24; bf16: 2^-133, whose first binade goes on where they end), so bytes and nibbles in place are
+// operands, a low nibble as c and a byte as c + 16 c': four instructions for eight codes (8 ragged requests 116 us; low
+// and high nibbles masked each: five, 121 us; nibbles shifted under exponent bits, with offsets of 16 to 256 to cancel:
+// six to eight, 139 us).  K: q c + q' c' = (q - q'/16) c + (q'/16) (c + 16 c'), so the queries go in as those, fp16 with a power
+// of two that makes up for 2^-24.  V: the row of bytes less the row of low nibbles, at the end; the weights are bf16, for
+// their range, and 2^64 times larger.  What is left is the levels' own 7.5: inside a tile's product for the logits, for P V
+// against the sum of the weights over all keys.
+// nibbles (2 h, 2 h + 4) and bytes (h, h + 2) of a word
+__device__ __forceinline__ void code_bytes(uint32_t w, int h, uint32_t& low, uint32_t& both) {
+  both = h ? __byte_perm(w, 0u, 0x4341) : w & 0x00FF00FFu;
+  low = (h ? both : w) & 0x000F000Fu;
+}
 // D = A B + C, m16n8k16, fp16 operands, fp32 sums
 __device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1, const float (&c)[4]) {
@@ -394,11 +400,12 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
       for (int kh = 0; kh < 2; ++kh) {
-        const float x0 = d[ks][kh].x * (kh ? up / 16.f : up), x1 = d[ks][kh].y * (kh ? up / 16.f : up);
+        const float x0 = kh ? d[ks][1].x * (up / 16.f) : fmaf(d[ks][1].x, -1.f / 16.f, d[ks][0].x) * up;
+        const float x1 = kh ? d[ks][1].y * (up / 16.f) : fmaf(d[ks][1].y, -1.f / 16.f, d[ks][0].y) * up;
         __half2 v = __floats2half2_rn(x0, x1);
         if (PACK && (r & 1)) v = __floats2half2_rn(x0 - __low2float(v), x1 - __high2float(v));
         qf[ks][kh] = h2_as_u32(v);
-        part[ks >> 2] = fmaf(kh ? -16.f * kOffset4 * kKUnit : -kOffset4 * kKUnit, __low2float(v) + __high2float(v), part[ks >> 2]);
+        part[ks >> 2] = fmaf(kh ? -17.f * kOffset4 * kKUnit : -kOffset4 * kKUnit, __low2float(v) + __high2float(v), part[ks >> 2]);
       }
     // sums over the column's four lanes, then to the lanes that hold columns 2 tq, 2 tq + 1 of the logits
 #pragma unroll
@@ -465,8 +472,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           uint32_t a0, a1, a2, a3;
-          code_pairs(word_of(w0, ks >> 1) >> (8 * (ks & 1)), a0, a2);
-          code_pairs(word_of(w1, ks >> 1) >> (8 * (ks & 1)), a1, a3);
+          code_bytes(word_of(w0, ks >> 1), ks & 1, a0, a2);
+          code_bytes(word_of(w1, ks >> 1), ks & 1, a1, a3);
           if ((ks & 3) == 0)  // the group's sum starts from the offset's part
             mma_f16_from(acc[ks >> 2], a0, a1, a2, a3, qf[ks][0], qf[ks][1], q0[ks >> 2]);
           else
@@ -600,8 +607,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
           for (int q = 0; q < 4; ++q) {
             const uint32_t wq = word_of(w, q);
             uint32_t a0, a1, a2, a3;
-            code_pairs(wq, a0, a1);
-            code_pairs(wq >> 8, a2, a3);
+            code_bytes(wq, 0, a0, a1);
+            code_bytes(wq, 1, a2, a3);
             mma_bf16_acc(st.o[4 * gr + q], a0, a1, a2, a3, bv[gr][0], bv[gr][1]);
           }
         }
@@ -646,14 +653,19 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
                           : 16 * mt + 8 * hf + r;
       if constexpr (PACK) {
         float y = st.o[mt][2 * hf] + st.o[mt][2 * hf + 1];
-        if constexpr (INT4) y = fmaf(-kOffset4 / kVUp, st.wsum[mt >> 2][0], y * (hf ? kVDown / 16.f : kVDown));
+        if constexpr (INT4) {
+          if (hf) y -= st.o[mt][0] + st.o[mt][1];
+          y = fmaf(-kOffset4 / kVUp, st.wsum[mt >> 2][0], y * (hf ? kVDown / 16.f : kVDown));
+        }
         if (tq < g) so[(warp * g + tq) * kD + ch] = y;
       } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float y = st.o[mt][2 * hf + e];
-          if constexpr (INT4)
+          if constexpr (INT4) {
+            if (hf) y -= st.o[mt][e];
             y = fmaf(-kOffset4 / kVUp, st.wsum[mt >> 2][e], y * (hf ? kVDown / 16.f : kVDown));
+          }
           if (2 * tq + e < g) so[(warp * g + 2 * tq + e) * kD + ch] = y;
         }
       }

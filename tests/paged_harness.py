@@ -83,7 +83,9 @@ def attention_error(out, q, K, V, spans, window, sinks, pack, sm_scale=128 ** -0
     pack: the weights enter their products as two bf16 terms (2^-16) instead of one (2^-8).
     held: 4-bit caches: per request (s_k, s_v) [n, Hkv], the largest scale of each row; then K and V are in the rotated
     basis, the query goes in as fp16 (half a step: 2^-11 of a channel; with pack a second term takes it below 2^-16) and
-    the levels' 7.5 cancels in fp32 against the codes, 0..15: terms of at most 22.5 scales for levels of 7.5.
+    two channels' codes are one operand, c + 16 c': q' / 16, whose rounding reaches c and 16 c', and q - q' / 16, whose
+    rounding reaches c: with levels of at most 7.5 scales |q'| 7.5 / 8 more than each channel's own part.  The levels' 7.5
+    cancels in fp32 against the codes: terms of at most 15 + 15 / 16 + 7.5 scales.
     """
     worst, i = 0.0, 0
     Hq = q.shape[1]
@@ -102,9 +104,10 @@ def attention_error(out, q, K, V, spans, window, sinks, pack, sm_scale=128 ** -0
                 if held is not None:
                     see = paged.visible(p, len(k), window, sinks)
                     sk, sv = (float(s[:ctx, h][see].max()) if see.any() else 0.0 for s in held[b])
-                    ex += ((2.0 ** -16 if pack else 2.0 ** -11) * X + 8 * 2.0 ** -23 * 22.5 * sk * np.abs(qr).sum()) * sm_scale
+                    r = 2.0 ** -16 if pack else 2.0 ** -11
+                    ex += (r * X + (r * 7.5 / 8 + 8 * 2.0 ** -23 * 23.5) * sk * np.abs(qr).sum()) * sm_scale
                     steps = len(k) / 16 + 8
-                    d = (w + 2 * ex) * A + (2.0 ** -16 + steps * 2.0 ** -23) * 22.5 * sv
+                    d = (w + 2 * ex) * A + (2.0 ** -16 + steps * 2.0 ** -23) * 23.5 * sv
                     o, slack = paged.from_rotated(o), np.full(128, d.sum() / np.sqrt(128.0))
                 else:
                     slack = (w + 2 * ex + (len(k) / 16) * 2.0 ** -23) * A
