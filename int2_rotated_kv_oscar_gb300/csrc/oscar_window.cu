@@ -507,8 +507,8 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
       }
     }
     // positions that the query does not see (or whose page is bad) drop out by selection
-    uint32_t hid = 0;  // bit 2 k + rh: token r + 8 rh of tile k
     if (bad || !((T >= in0 || 16 * (T + KU) <= s.sinks) && T + KU <= in1)) {
+      uint32_t hid = 0;  // bit 2 k + rh: token r + 8 rh of tile k
 #pragma unroll
       for (int k = 0; k < KU; ++k)
 #pragma unroll
@@ -521,6 +521,13 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
 #pragma unroll
           for (int e = 0; e < kH; ++e)
             if ((hid >> (2 * k + rh)) & 1u) x[k][rh][e] = -INFINITY;
+      if constexpr (INT4) {  // a V row nobody wrote may hold any scale: 0 in the stage
+#pragma unroll
+        for (int i = 0; i < 2 * KU; ++i)
+          if (tq == 0 && ((hid >> i) & 1u))
+            asm volatile("st.shared.b32 [%0], 0;\n" ::"r"(stage + (i >> 1) * kTile4Bytes + kTile4Scales + 64 + 4 * (r + 8 * (i & 1))) : "memory");
+        __syncwarp();
+      }
     }
     // running maximum; the accumulators move only when it grew a lot
     float sub[kH];
@@ -574,10 +581,9 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
         }
         if constexpr (INT4) {
           const uint32_t u = lds32(stage + k * kTile4Bytes + kTile4Scales + 64 + 4 * (r + 8 * rh));
-          float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&u));
+          const float2 sc = __half22float2(*reinterpret_cast<const __half2*>(&u));
 #pragma unroll
           for (int e = 0; e < kH; ++e) p[e] *= kVUp;
-          if ((hid >> (2 * k + rh)) & 1u) sc = make_float2(0.f, 0.f);  // a row nobody wrote may hold any scale
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
             const float sg = gr ? sc.y : sc.x;
