@@ -32,9 +32,9 @@ constexpr float kLog2eW = 1.4426950408889634f;
 constexpr float kLazyW = 8.0f;  // the accumulators are rescaled when the maximum grows by more than 2^8
 
 // WIDE: 16 warps and one block per SM (4 bits), for few pairs, whose cuts each cost a join (batch 1 x 100K, 8
-// pairs: 27.5 us, 30.4 us with two blocks of 8); else two blocks of 8, one of which copies and computes while the
-// other begins or joins a segment (28 requests x 4160 visible keys, 224 pairs: 35.9 us against 41.7; 8 ragged
-// requests, 64 pairs: 126 against 131).  BF16 has one block of 8 (its units are larger).
+// pairs: 27.1 us, 29.6 us with two blocks of 8); else two blocks of 8, one of which copies and computes while the
+// other begins or joins a segment (28 requests x 4160 visible keys, 224 pairs: 34.5 us against 41.0; 8 ragged
+// requests, 64 pairs: 115 against 120).  BF16 has one block of 8 (its units are larger).
 template <bool INT4, bool WIDE>
 struct Ring {
   static constexpr int kWarps = INT4 && WIDE ? 16 : 8;
@@ -165,7 +165,7 @@ struct State {
 
 // 4-bit words to operands: the low byte of a 16-bit float without any exponent bits is a whole number of its smallest
 // subnormals (fp16: 2^-24; bf16: 2^-133, whose first binade goes on where they end), so bytes and nibbles in place are
-// operands, a low nibble as c and a byte as c + 16 c': four instructions for eight codes (8 ragged requests 116 us; low
+// operands, a low nibble as c and a byte as c + 16 c': four instructions for eight codes (8 ragged requests 115 us; low
 // and high nibbles masked each: five, 121 us; nibbles shifted under exponent bits, with offsets of 16 to 256 to cancel:
 // six to eight, 139 us).  K: q c + q' c' = (q - q'/16) c + (q'/16) (c + 16 c'), so the queries go in as those, fp16 with a power
 // of two that makes up for 2^-24.  V: the row of bytes less the row of low nibbles, at the end; the weights are bf16, for
