@@ -134,8 +134,9 @@ __global__ void __launch_bounds__(128) append_bf16_kernel(AppendLaunch a) {
   // Evicting: the tile kernel after this one may start (it touches no BF16
   // row), and the ring rows written here are the ones the eviction kernel
   // before this one reads, so wait for it first.  Fresh ring: this kernel
-  // runs beside the tile kernel before it and waits for it at the end, so
-  // that its end marks the call's.
+  // runs beside the tile kernel before it, which lets it go once the work
+  // before the call is complete (that may have written K and V, or read the
+  // ring's rows), and waits for it at the end, so that its end marks the call's.
   const bool fresh = (a.flags & 1u) != 0;
   griddep_launch_dependents();
   if (!fresh) griddep_wait();
@@ -237,8 +238,9 @@ __device__ __forceinline__ uint32_t sw128_offset(int row, int ch) {
 __global__ void __launch_bounds__(kTcThreads, 1)
     append_tile_kernel(const __grid_constant__ AppendLaunch a, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, unsigned tiles2, unsigned nv) {
-  // the kernel after this one may start beside it (it waits before it reads what this one writes)
-  griddep_launch_dependents();
+  // the kernel after this one may start beside it (it waits before it reads what this one writes); for a fresh
+  // prompt that is the call's BF16-row kernel, which must not start before the work ahead of the call is complete
+  if (!(a.flags & 1u)) griddep_launch_dependents();
   extern __shared__ uint8_t tc_raw[];
   const uint32_t raw_s = smem_u32(tc_raw);
   uint8_t* sm = tc_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
@@ -300,7 +302,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // For a fresh prompt this kernel comes first in the call and may start before the stream's
   // previous work has finished: the set-up above reads only the rotation tables (written by a
   // synchronous upload), so wait here, before the inputs, tables and page blocks are touched.
-  if (a.flags & 1u) griddep_wait();
+  if (a.flags & 1u) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
 
   if (warp == 16) {
     // x tiles by TMA; after the last tile a buffer with work = 0 tells the MMA thread to stop.  The
@@ -606,7 +611,7 @@ cudaError_t launch_append(const AppendLaunch& a, cudaStream_t stream) {
   // BF16-row kernels do not touch; the eviction reads ring rows that the
   // BF16-row kernel overwrites.
   //   evicting:     eviction -> BF16 rows (wait first) -> tiles (wait at the end)
-  //   fresh ring:   tiles (set-up, then wait) -> BF16 rows (wait at the end)
+  //   fresh ring:   tiles (set-up, wait, then let go) -> BF16 rows (wait at the end)
   // so the last kernel of the call always ends after the others.
   AppendLaunch la = a;
   void* args1[] = {&la};

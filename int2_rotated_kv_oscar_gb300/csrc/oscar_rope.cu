@@ -98,8 +98,7 @@ __device__ __forceinline__ void rope_rows(const RopeLaunch& a, int block, int b,
 
 template <int TURN>
 __global__ void __launch_bounds__(256) rope_append_bf16_kernel(const __grid_constant__ RopeLaunch a, int split) {
-  // (no early launch of what comes next: the mixed cache's append of a fresh prompt reads its K and V beside the kernel
-  // before it, and they may be this one's q_out)
+  // (no early launch of what comes next: it gained nothing)
   griddep_wait();
   rope_rows<TURN, true, 256>(a, blockIdx.x, blockIdx.y, split);
 }
