@@ -113,7 +113,8 @@ __device__ __forceinline__ bool seen_by(const WindowLaunch& a, int i, int& b, Se
     len = limit;
   }
   s.len = (int)len;
-  s.low = a.window < 0 ? 0 : (int)min(max(p + 1 - a.window, 0ll), (long long)INT32_MAX);
+  // (not beyond the length: nothing there is held, and roundings of a low near 2^31 would overflow)
+  s.low = a.window < 0 ? 0 : (int)min(max(p + 1 - a.window, 0ll), len);
   s.sinks = min(a.sinks, s.len);
   // in units of KU tiles, so that a unit never straddles two pages
   constexpr int kTok = 16 * KU;
