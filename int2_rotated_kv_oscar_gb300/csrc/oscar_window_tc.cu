@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
       if (fk > 0.f) y = make_float4(fmaf(u.x, fk, y.x), fmaf(u.y, fk, y.y), fmaf(u.z, fk, y.z), fmaf(u.w, fk, y.w));
     }
   }
-  const float f = L > 0.f ? 1.f / L : 0.f;
+  const float f = L == 0.f ? 0.f : 1.f / L;  // (a sum that is not a number reaches the row: its terms above were left out)
   reinterpret_cast<uint2*>(a.out + ((size_t)(row0 + pair * 2 * ta.qpt + q) * a.Hq + h * g + head) * kD)[lane] =
       make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
 }
