@@ -215,7 +215,7 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   __shared__ int pre[kMaxRows + 1], scan[kW];
   griddep_wait();
   griddep_launch_dependents();  // (behind the wait: what is before this kernel is complete once the next one starts)
-  const int g = a.Hq / a.Hkv, rows = a.tok.n_tokens, block = blockIdx.x;
+  const int g = a.Hq / a.Hkv, rows = a.tok.n_tokens, G = gridDim.x, block = blockIdx.x;
   const bool few = rows <= 32;  // each warp adds the rows up for itself, lane i row i
   int at = 0, end = 1, total = 0;  // this block's range of all units
   int pre_l = 0, units_l = 0;                // few: units before row `lane` (of one KV head), and its own
@@ -270,17 +270,13 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
     }
     total *= a.Hkv;
     // queries that see nothing get zeros
-    for (int i = block; i < rows; i += gridDim.x) {
+    for (int i = block; i < rows; i += G) {
       const int n = few ? __shfl_sync(0xffffffffu, units_l, i) : pre[i + 1] - pre[i];
       if (n == 0 && seen_by<KU>(a, i, b, s, false))
         for (int c = threadIdx.x; c < a.Hq * (kD / 8); c += 32 * kW)
           reinterpret_cast<uint4*>(a.out + (size_t)i * a.Hq * kD)[c] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  // The blocks that share the units.  The host sized the grid from its bound of the lengths; fewer units than blocks
-  // would leave ranges without any inside a pair, whose blocks add nothing to the pair's counter but lie between its
-  // first and last.  Then as many blocks as have a unit for each warp, so that a range is a unit or longer.
-  const int G = total >= (int)gridDim.x ? (int)gridDim.x : max(1, (total + kW - 1) / kW);
   // the pair that unit x belongs to: its row, KV head, first unit and units
   auto pair_of = [&](int x, int& row, int& h, int& units) {
     int before;
@@ -308,8 +304,12 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   };
   // where block k's range begins: near the k-th of G equal parts (a product of floats: the same everywhere and
   // monotonic in k, which is all that matters), or at the pair's edge when that is at most kSlack units away (a
-  // segment costs as much as several units of every warp)
-  const float step = (float)total / (float)G;
+  // segment costs as much as several units of every warp).  G is the grid, which the host sized from its bound of the
+  // lengths; but when there are fewer units than blocks, as many blocks as have a unit for each warp, since a range
+  // without units inside a pair would be one whose block adds nothing to the pair's counter and yet lies between the
+  // pair's first and last (the rest begin at `total`: a little more than total / G takes the product past it)
+  const float step = total >= G ? (float)total / (float)G
+                                : (float)total / (float)max(1, (total + kW - 1) / kW) * (1.f + 1.f / (1 << 20));
   auto begin_of = [&](int k) {
     const int x = k >= G ? total : min(total, (int)(step * (float)k));
     if (x == 0 || x >= total) return x;
