@@ -206,6 +206,15 @@ def _ptr(x):
     return x.data_ptr()
 
 
+def _tensor(x, dtype, name, dims=1, at_least=0):
+    """Address of x; a tensor (not an address) must be contiguous, of this type and dimensions, and long enough."""
+    if x is not None and not isinstance(x, int):
+        if str(x.dtype) != "torch." + dtype or not x.is_contiguous() or x.dim() != dims or x.shape[0] < at_least:
+            raise ValueError("%s must be a contiguous %s tensor of %d dimension(s), %d entries or more"
+                             % (name, dtype, dims, at_least))
+    return _ptr(x)
+
+
 def _stream(stream):
     if stream is None:
         return None
@@ -312,7 +321,7 @@ def oscar_calib_clip_threshold(ctx, x, n_rows, U, flags, percentile, workspace, 
 
 def oscar_rope_table(ctx, table, theta, stream=None):
     """Fill a device float32 table [n_positions, rotary_dim] with cos and sin of the position angles."""
-    _check(load().oscar_rope_table(ctx, _ptr(table), table.shape[0], table.shape[1], float(theta), _stream(stream)),
+    _check(load().oscar_rope_table(ctx, _tensor(table, "float32", "table", dims=2), table.shape[0], table.shape[1], float(theta), _stream(stream)),
            "oscar_rope_table")
 
 
@@ -330,8 +339,9 @@ def oscar_rope_append_int4(ctx, view, args, stream=None):
 
 def oscar_int4_to_bf16(ctx, from_view, to_view, pos, count, max_count, stream=None):
     """Read positions [pos, pos + count) of every request (device int32) back from the 4-bit cache into BF16 pages."""
-    _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), _ptr(pos), _ptr(count),
-                                     max_count, _stream(stream)), "oscar_int4_to_bf16")
+    pos, count = (_tensor(x, "int32", name, at_least=from_view.batch) for x, name in ((pos, "pos"), (count, "count")))
+    _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), pos, count, max_count,
+                                     _stream(stream)), "oscar_int4_to_bf16")
 
 
 def oscar_window_workspace_bytes(ctx):

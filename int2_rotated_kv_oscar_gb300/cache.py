@@ -185,6 +185,15 @@ def _types(*groups):
             device = t.device
 
 
+def _requests(n_tokens, cu_seqlens, *tensors):
+    """One entry for each request in each of the tensors: the kernels read as many as the call has requests."""
+    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.shape[0] == 0):
+        raise ValueError("cu_seqlens must be [batch + 1]")
+    batch = n_tokens if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if any(t.dim() != 1 or t.shape[0] < batch for t in tensors):
+        raise ValueError("%d requests need as many positions and lengths" % batch)
+
+
 def _token_stride(x, name):
     """Elements from one token to the next of x [n_tokens, heads, 128], whose rows of a token must be packed."""
     if x.dim() != 3 or x.shape[2] != abi.HEAD_DIM or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != abi.HEAD_DIM):
@@ -210,6 +219,7 @@ def rope_append_args(k, v, pos, q=None, q_out=None, rope=None, interleaved=False
     if v.shape != k.shape or (q is None) != (q_out is None) or (
             q is not None and (q.shape[0] != n or q_out.shape != q.shape)) or (rope is not None and rope.dim() != 2):
         raise ValueError("k and v, and q and q_out, must have one shape and n_tokens rows, rope two dimensions")
+    _requests(n, cu_seqlens, pos)
     a = abi.oscar_rope_append_args(
         q=None if q is None else q.data_ptr(), q_out=None if q_out is None else q_out.data_ptr(), k=k.data_ptr(),
         v=v.data_ptr(), q_stride=0 if q is None else _token_stride(q, "q"),
@@ -232,6 +242,7 @@ def window_args(q, out, pos, ctx_len, max_ctx_len, window=-1, sinks=0, cu_seqlen
     _contiguous(*(t for t in (out, pos, ctx_len, cu_seqlens) if t is not None))
     if out.shape != q.shape:
         raise ValueError("q and out must have one shape")
+    _requests(n, cu_seqlens, pos, ctx_len)
     a = abi.oscar_window_args(
         q=q.data_ptr(), out=out.data_ptr(), pos=pos.data_ptr(),
         cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr(), ctx_len=ctx_len.data_ptr(),
