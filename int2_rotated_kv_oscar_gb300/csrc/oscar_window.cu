@@ -37,10 +37,11 @@ namespace {
 constexpr float kLog2eW = 1.4426950408889634f;
 constexpr float kLazyW = 8.0f;  // the accumulators are rescaled when the maximum grows by more than 2^8
 
-// WIDE: 16 warps and one block per SM (4 bits), for few pairs, whose cuts each cost a join (batch 1 x 100K, 8
-// pairs: 27.1 us, 29.6 us with two blocks of 8); else two blocks of 8, one of which copies and computes while the
-// other begins or joins a segment (28 requests x 4160 visible keys, 224 pairs: 34.5 us against 41.0; 8 ragged
-// requests, 64 pairs: 115 against 120).  BF16 has one block of 8 (its units are larger).
+// WIDE: 16 warps and one block per SM (4 bits), for few pairs, whose cuts each cost a join (8 pairs x 100K keys:
+// 26.9 us, 29.5 us with two blocks of 8; x 32K 16.4, 18.6; but x 4K 13.4, 11.5); else two blocks of 8, one of which
+// copies and computes while the other begins or joins a segment (9 pairs x 100K 35.9 us, 38.1 wide; 16 pairs 44.2, 51.6;
+// 24 pairs 63.9, 66.5; 64 pairs of ragged lengths 115, 120; 224 pairs x 4160 visible keys 34.5, 41.0).  From 9 pairs on
+// only calls of about 1000 keys are a microsecond faster wide.  BF16 has one block of 8 (its units are larger).
 template <bool INT4, bool WIDE>
 struct Ring {
   static constexpr int kWarps = INT4 && WIDE ? 16 : 8;
@@ -50,7 +51,9 @@ struct Ring {
   static constexpr int kStages = 3;
   static constexpr int kBytes = kWarps * kStages * kUnit;
 };
-constexpr int kWidePairs = 32;  // (query, KV head) pairs from which on the blocks are the smaller ones
+constexpr int kWidePairs = 9;  // (query, KV head) pairs from which on the blocks are the smaller ones
+// Units at a pair's ends that go to the neighbouring range (8 pairs x 100K keys: 27.4 us with 2 to 32, 34.9 us with
+// none; 104 pairs x 1000 18.7 us with 4 or less, 14.2 with 8, 12.7 with 16; 224 pairs x 4160 35.7, 36.0 with 32)
 constexpr int kSlack = 8;
 constexpr int kMaxRows = 1024;  // query rows whose lengths a block adds up; with more, a block takes one whole pair
 
