@@ -206,15 +206,6 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _tensor(x, dtype, name, dims=1, at_least=0):
-    """Address of x; a tensor (not an address) must be contiguous, of this type and dimensions, and long enough."""
-    if x is not None and not isinstance(x, int):
-        if str(x.dtype) != "torch." + dtype or not x.is_contiguous() or x.dim() != dims or x.shape[0] < at_least:
-            raise ValueError("%s must be a contiguous %s tensor of %d dimension(s), %d entries or more"
-                             % (name, dtype, dims, at_least))
-    return _ptr(x)
-
-
 def _stream(stream):
     if stream is None:
         return None
@@ -321,7 +312,9 @@ def oscar_calib_clip_threshold(ctx, x, n_rows, U, flags, percentile, workspace, 
 
 def oscar_rope_table(ctx, table, theta, stream=None):
     """Fill a device float32 table [n_positions, rotary_dim] with cos and sin of the position angles."""
-    _check(load().oscar_rope_table(ctx, _tensor(table, "float32", "table", dims=2), table.shape[0], table.shape[1], float(theta), _stream(stream)),
+    if str(table.dtype) != "torch.float32" or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("the table must be a contiguous float32 tensor [n_positions, rotary_dim]")
+    _check(load().oscar_rope_table(ctx, _ptr(table), table.shape[0], table.shape[1], float(theta), _stream(stream)),
            "oscar_rope_table")
 
 
@@ -337,9 +330,27 @@ def oscar_rope_append_int4(ctx, view, args, stream=None):
            "oscar_rope_append_int4")
 
 
+_int32 = None  # torch.int32, once a tensor has been seen (naming a type takes as long as a launch)
+
+
+def _is_int32(dtype):
+    global _int32
+    if str(dtype) == "torch.int32":
+        _int32 = dtype
+    return dtype is _int32
+
+
 def oscar_int4_to_bf16(ctx, from_view, to_view, pos, count, max_count, stream=None):
     """Read positions [pos, pos + count) of every request (device int32) back from the 4-bit cache into BF16 pages."""
-    pos, count = (_tensor(x, "int32", name, at_least=from_view.batch) for x, name in ((pos, "pos"), (count, "count")))
+    if pos is not None and pos.__class__ is not int:  # a tensor, not an address
+        if (pos.dtype is not _int32 and not _is_int32(pos.dtype)) or pos.numel() < from_view.batch or not pos.is_contiguous():
+            raise ValueError("pos must be a contiguous int32 tensor with an entry for each request")
+        pos = pos.data_ptr()
+    if count is not None and count.__class__ is not int:
+        if (count.dtype is not _int32 and not _is_int32(count.dtype)) or count.numel() < from_view.batch or (
+                not count.is_contiguous()):
+            raise ValueError("count must be a contiguous int32 tensor with an entry for each request")
+        count = count.data_ptr()
     _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), pos, count, max_count,
                                      _stream(stream)), "oscar_int4_to_bf16")
 
