@@ -22,9 +22,9 @@
 // What bounds it: BF16 the copies (64 requests x 4100 visible keys of 8 heads,
 // 1.07 GB: 166 us, 95% of the copy bandwidth); 4 bits in part the instructions
 // that make operands of the codes, about 240 for 16 tokens (8 ragged requests of
-// 8K to 128K tokens, 657 MB: 115 us, 84%), and for short calls the way in
+// 8K to 128K tokens, 657 MB: 118 us, 82%), and for short calls the way in
 // (positions, page table, first copies: 6 us) and out (the join: 5 us): batch 1 x
-// 100K, 109 MB, 27.1 us, of which the loop takes 15.
+// 100K, 109 MB, 27.4 us, of which the loop takes 15.
 
 #include "oscar_paged.cuh"
 
@@ -38,10 +38,10 @@ constexpr float kLog2eW = 1.4426950408889634f;
 constexpr float kLazyW = 8.0f;  // the accumulators are rescaled when the maximum grows by more than 2^8
 
 // WIDE: 16 warps and one block per SM (4 bits), for few pairs, whose cuts each cost a join (8 pairs x 100K keys:
-// 26.9 us, 29.5 us with two blocks of 8; x 32K 16.4, 18.6; but x 4K 13.4, 11.5); else two blocks of 8, one of which
-// copies and computes while the other begins or joins a segment (9 pairs x 100K 35.9 us, 38.1 wide; 16 pairs 44.2, 51.6;
-// 24 pairs 63.9, 66.5; 64 pairs of ragged lengths 115, 120; 224 pairs x 4160 visible keys 34.5, 41.0).  From 9 pairs on
-// only calls of about 1000 keys are a microsecond faster wide.  BF16 has one block of 8 (its units are larger).
+// 27.4 us, 29.8 us with two blocks of 8; x 32K 16.4, 18.8; but x 4K 13.6, 11.7); else two blocks of 8, one of which
+// copies and computes while the other begins or joins a segment (9 pairs x 100K 36.3 us, 38.6 wide; 16 pairs 44.2, 52.4;
+// 24 pairs 63.5, 66.9; 64 pairs of ragged lengths 118, 123; 224 pairs x 4160 visible keys 35.0, 41.3).  From 9 pairs on
+// only calls of about 1000 keys are faster wide, by up to 2 us.  BF16 has one block of 8 (its units are larger).
 template <bool INT4, bool WIDE>
 struct Ring {
   static constexpr int kWarps = INT4 && WIDE ? 16 : 8;
@@ -52,8 +52,8 @@ struct Ring {
   static constexpr int kBytes = kWarps * kStages * kUnit;
 };
 constexpr int kWidePairs = 9;  // (query, KV head) pairs from which on the blocks are the smaller ones
-// Units at a pair's ends that go to the neighbouring range (8 pairs x 100K keys: 27.4 us with 2 to 32, 34.9 us with
-// none; 104 pairs x 1000 18.7 us with 4 or less, 14.2 with 8, 12.7 with 16; 224 pairs x 4160 35.7, 36.0 with 32)
+// Units at a pair's ends that go to the neighbouring range (8 pairs x 100K keys: 27.4 us with 4 to 16, 35.4 us with
+// none; 104 pairs x 1000 18.6 us with 4 or none, 14.2 with 8, 12.5 with 16; 224 pairs x 4160 35.0, 35.2 with 16)
 constexpr int kSlack = 8;
 constexpr int kMaxRows = 1024;  // query rows whose lengths a block adds up; with more, a block takes one whole pair
 
@@ -175,7 +175,7 @@ struct State {
 
 // 4-bit words to operands: the low byte of a 16-bit float without any exponent bits is a whole number of its smallest
 // subnormals (fp16: 2^-24; bf16: 2^-133, whose first binade goes on where they end), so bytes and nibbles in place are
-// operands, a low nibble as c and a byte as c + 16 c': four instructions for eight codes (8 ragged requests 115 us; low
+// operands, a low nibble as c and a byte as c + 16 c': four instructions for eight codes (8 ragged requests 115 us then; low
 // and high nibbles masked each: five, 121 us; nibbles shifted under exponent bits, with offsets of 16 to 256 to cancel:
 // six to eight, 139 us).  K: q c + q' c' = (q - q'/16) c + (q'/16) (c + 16 c'), so the queries go in as those, fp16 with a power
 // of two that makes up for 2^-24.  V: the row of bytes less the row of low nibbles, at the end; the weights are bf16, for
