@@ -198,7 +198,12 @@ def _token_stride(x, name):
     """Elements from one token to the next of x [n_tokens, heads, 128], whose rows of a token must be packed."""
     if x.dim() != 3 or x.shape[2] != abi.HEAD_DIM or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != abi.HEAD_DIM):
         raise ValueError("%s must be [n_tokens, heads, 128] with packed heads" % name)
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * abi.HEAD_DIM
+    row = x.shape[1] * abi.HEAD_DIM
+    if x.shape[0] <= 1:
+        return row
+    if x.stride(0) < row:  # (0, a row broadcast to all tokens, would mean packed rows)
+        raise ValueError("the rows of %s must not overlap" % name)
+    return x.stride(0)
 
 
 def rope_table(ctx, n_positions, rotary_dim=128, theta=1e6, device="cuda"):

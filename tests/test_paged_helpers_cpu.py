@@ -64,3 +64,19 @@ def test_the_4_bit_cache_as_a_class():
     assert (v.num_pages, v.max_pages_per_req, v.batch) == (5, 4, 3)
     assert (v.pages, v.page_table) == (c.pages.data_ptr(), c.page_table.data_ptr())
     assert not c.pages.any() and c.pages.shape == (5, 2, abi.INT4_BLOCK_BYTES)
+
+
+def test_rows_that_share_memory():
+    """One row broadcast to all tokens has a stride of 0, which the structs take for packed rows."""
+    q = torch.zeros(3, 4, 128, dtype=torch.bfloat16)
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    assert kv.window_args(q[:1].expand(1, 4, 128), q[:1].clone(), ints(1), ints(1), 10).q_stride == 512
+    with pytest.raises(ValueError):
+        kv.window_args(q[:1].expand(3, 4, 128), q.clone(), ints(3), ints(3), 10)
+    rows = torch.zeros(3 * 256 + 256, dtype=torch.bfloat16)
+    for bad in (k[:1].expand(3, 2, 128), rows.as_strided((3, 2, 128), (128, 128, 1))):
+        for change in (dict(k=bad), dict(v=bad), dict(q=bad, q_out=k.clone()), dict(q=k.clone(), q_out=bad)):
+            a = dict(k=k, v=k.clone(), pos=ints(3))
+            a.update(change)
+            with pytest.raises(ValueError):
+                kv.rope_append_args(**a)
