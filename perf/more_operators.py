@@ -201,7 +201,8 @@ def prepare(case, seed):
             s[name + "_sink"] = outliers(randn(batch, PAGE, hkv, D)).to(torch.bfloat16).transpose(1, 2).contiguous()
             s[name + "_ring"] = outliers(randn(batch, RECENT, hkv, D)).to(torch.bfloat16).transpose(1, 2).contiguous()
             s[name + "_pages"] = torch.zeros((n_pages, hkv, PAGE, D), dtype=torch.bfloat16, device=dev)
-        s["rotation"] = torch.from_numpy(_rotation()[1]).to(dev)
+        s["u"], rotation = _rotation()
+        s["rotation"] = torch.from_numpy(rotation).to(dev)
         return s
 
     hq, n = case["hq"], s["n"]
@@ -243,8 +244,6 @@ def _plan(s):
         _contexts[heads] = abi.oscar_create(abi.oscar_config(
             num_layers=1, num_q_heads=heads[0], num_kv_heads=heads[1], head_dim=D, page_size=PAGE, sink=SINK,
             recent=RECENT, group=64, device=torch.cuda.current_device()))
-        u = _rotation()[0]
-        abi.oscar_load_rotation(_contexts[heads], 0, u, u, 30.0, 30.0)
     p = dict(ctx=_contexts[heads], abi=abi)
     if c["op"] == "table":
         p["scaling"] = None if c["scaling"] == "none" else kv.rope_scaling(
@@ -261,6 +260,7 @@ def _plan(s):
                                    sinks=c["sinks"])
         p["workspace"] = kv.window_workspace(p["ctx"])
     else:
+        abi.oscar_load_rotation(p["ctx"], 0, s["u"], s["u"], 30.0, 30.0)
         p["from"] = abi.oscar_cache_view(
             int2_pages=s["int2"].data_ptr(), num_pages=s["int2"].shape[0], k_sink=s["k_sink"].data_ptr(),
             v_sink=s["v_sink"].data_ptr(), num_sink_pages=c["batch"], k_ring=s["k_ring"].data_ptr(),
