@@ -921,7 +921,8 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
           if (!whole) {
             const int base = block_page<ROWS>(ta, my, k0 + hf, bad), sinks = my.sinks;
             const int p = min(my.p0 + my.i0 + max(ql, 0), my.last);
-            const int lim = min(p + 1, my.ctx), low = a.window < 0 ? 0 : max(0, p - a.window + 1);
+            // (over packed rows p may be below -1: lim - p32 would leave 32 bits at a page that is not there)
+            const int lim = max(0, min(p + 1, my.ctx)), low = a.window < 0 ? 0 : max(0, p - a.window + 1);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int p32 = base + 32 * k;
