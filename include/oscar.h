@@ -594,8 +594,8 @@ oscar_status oscar_int4_to_bf16(oscar_ctx* ctx, const oscar_int4_cache_view* fro
  * Cache rows that no query of the call sees may hold anything, NaN included.
  * A V row that is not finite may reach, beside the queries that see it, others
  * of its request (their tile of 128 rows).  The sums may run up to 2^50 times
- * larger than the result before their division, so values of V beyond 2^77
- * may overflow.
+ * larger than the result before their division, however many keys there are,
+ * so values of V beyond 2^77 may overflow.
  */
 typedef struct {
   const void* q;

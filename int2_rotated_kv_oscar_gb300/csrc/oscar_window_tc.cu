@@ -84,13 +84,14 @@ constexpr uint32_t kTcwItems = kTcwBars + 256;  // the softmax warps' items: [ti
 constexpr uint32_t kTcwX = kTcwBars + 1024;      // what the two halves of a row tell each other: [tile][half][128 rows] float
 constexpr size_t kTcwSmem = kTcwX + 2048;        // (all of it dynamic, so that it begins where the block's memory does)
 constexpr uint32_t kTmS = 0, kTmO = 256;         // TMEM columns of S and O, 128 a tile
-// A row's weights are taken relative to the maximum of the first block that it saw something of, until half a
-// block's sum of them reaches kTopSum (2^40; fp32 and bf16 reach 2^127): then the maximum is found anew, and O
-// and l move.  So the common block needs no maximum: its exponentials start with the first logits that arrive
-// (a block that moves takes 2000 cycles more; at 2^16 every fifth block did).
+// A row's weights are taken relative to the maximum of the first block that it saw something of, until half a row's
+// sum of them, over all blocks so far, reaches kTopSum (2^40; fp32 and bf16 reach 2^127): then the maximum is found
+// anew, or taken 2^39 higher if the sum was that already, and O and l move.  So the common block needs no maximum: its exponentials
+// start with the first logits that arrive (a block that moves takes 2000 cycles more; at 2^16 every fifth block did).
+// A record's sum stays below 2^41, and 304 records' below 2^50.
 constexpr float kTopSum = 1099511627776.0f;
-// Over packed rows the first block asks for no maximum either: weights are relative to 0 (what logits are near) until a
-// half block's sum reaches kTopSum, or a row that has seen something has less than 2^-60 of weight; then its maximum
+// Over packed rows the first block asks for no maximum either: weights are relative to 0 (what logits are near) until
+// half a row's sum reaches kTopSum, or a row that has seen something has less than 2^-60 of weight; then its maximum
 // becomes the reference, up or down (48 prompts of 1 to 2048 tokens 518 us then; 540 with a maximum found in each first block).
 constexpr float kLowSum = 8.673617379884035e-19f;
 constexpr int kRowFloats = kD + 2;               // of a tile's record, for each of its 128 rows: O[128], m, l
@@ -440,7 +441,7 @@ __device__ __forceinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it,
     // the records: O [row][128], then m [row], l [row]
     float* rec = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)it.record * 256 + 128 * t) * kRowFloats;
     if (live && hf == 0) {
-      rec[128 * kD + row] = got && l != 0.f ? m : -INFINITY;  // (over packed rows what saw nothing has a reference too)
+      rec[128 * kD + row] = got && l > 0.f ? m : -INFINITY;  // (over packed rows what saw nothing has a reference too)
       rec[129 * kD + row] = l;
     }
     if (got)
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
         }
         // (rows that are no query's hold leftovers: they never ask)
         const bool low = ROWS ? !anchored && l + sum.x + sum.y < kLowSum : m == -INFINITY;
-        const bool move = live && (!(sum.x + sum.y < kTopSum) || (low && (seen[0] | seen[1]) != 0));
+        const bool move = live && (!(l + sum.x + sum.y < kTopSum) || (low && (seen[0] | seen[1]) != 0));
         if ((!ROWS && j == 0) || pair_any(pair_bar, move)) {
           // the logits are still in place: the rows' maxima anew, O and l along, and the weights again
           uint32_t s[16];
@@ -966,12 +967,13 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
             hide(s, (k & 2 ? seen[1] : seen[0]) >> (16 * (k & 1)), 0);
             mb = fmaxf(mb, max16(s));
           }
+          if (l >= 0.5f * kTopSum) mb = fmaxf(mb, m + __fdividef(39.f, c));  // (many keys, of which none stands out)
           const uint32_t mine = sbase + kTcwX + 4 * (256 * t + 128 * hf + 32 * (warp & 3) + lane_id()), theirs = mine ^ 512u;
           sm_store(mine, __float_as_int(mb));
           group_sync(pair_bar, 64);
           mb = fmaxf(mb, __int_as_float(sm_load(theirs)));
           float f = 1.f;
-          // (a half's sum of kTopSum holds a weight of 2^34 at least, so the row that asked for it does move)
+          // (the row that asked for it does move: its sum was 2^39, or this block's is and holds a weight of 2^33)
           if constexpr (ROWS) {  // (both halves decide alike: by the row's maximum, and by its weight so far)
             group_sync(pair_bar, 64);
             sm_store(mine, __float_as_int(l));
