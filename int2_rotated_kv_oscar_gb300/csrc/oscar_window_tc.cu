@@ -69,6 +69,7 @@
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <math_constants.h>
 
 namespace oscar {
 namespace {
@@ -349,6 +350,20 @@ __device__ __forceinline__ int block_page(const TcwArgs& ta, const TcwItem& it, 
   return lp < 0 || (!ROWS && bad && page_of(ta.a.pages, it.b, lp, ta.a.err, false) < 0) ? INT32_MAX - 63 : lp * kPage;
 }
 
+// Whether query ql of an item (of the first of its keys' parts) sees any key: one that does and has no weight has logits of
+// -infinity alone, which is not a number as a row; one that does not gets zeros.
+template <bool ROWS>
+__device__ __forceinline__ bool row_sees(const TcwArgs& ta, const TcwItem& it, int ql, bool bad) {
+  const int p = min(it.p0 + it.i0 + ql, it.last), lim = min(p + 1, it.ctx);
+  const int low = ta.a.window < 0 ? 0 : max(0, p - ta.a.window + 1);
+  if (ROWS || !bad) return lim > 0 && (it.sinks > 0 || low < lim);
+  for (int k = 0; k < it.np; ++k) {
+    const int base = block_page<ROWS>(ta, it, k, true);
+    if (base < lim && (base < it.sinks || low < min(base + kPage, lim))) return true;
+  }
+  return false;
+}
+
 // V rows of a block that no query of the item sees may hold anything, and 0 x NaN is not 0: they become zeros, in
 // front of the products that read them.  One warp, 16 bytes a lane: four rows of 64 channels a step, by 32 rows' bits (with
 // a comparison of positions a row it took longer than the weights that it runs beside, and every item's last block
@@ -415,7 +430,7 @@ __device__ __forceinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it,
   const uint32_t rows = __ballot_sync(0xffffffffu, live);
   uint4 x[4];
   if constexpr (!SPLIT) {
-    const float f = got && l > 0.f ? 1.f / l : 0.f;
+    const float f = got && l != 0.f ? 1.f / l : 0.f;
     // the rows of the result [token][query head], in quarters of 64 bytes
     // (head row - (ql - t qpt) g of the KV head's; divisions by g here took 300 cycles an item)
     const uint32_t mine = (uint32_t)(it.row0 + it.i0 + ql) * a.Hq + (it.h - ql + t * ta.qpt) * g + row;
@@ -441,7 +456,7 @@ __device__ __forceinline__ void tcw_result(const TcwArgs& ta, const TcwItem& it,
     // the records: O [row][128], then m [row], l [row]
     float* rec = reinterpret_cast<float*>(a.workspace + a.plan.off_records) + ((size_t)it.record * 256 + 128 * t) * kRowFloats;
     if (live && hf == 0) {
-      rec[128 * kD + row] = got && l > 0.f ? m : -INFINITY;  // (over packed rows what saw nothing has a reference too)
+      rec[128 * kD + row] = got && l != 0.f ? m : -INFINITY;  // (over packed rows what saw nothing has a reference too)
       rec[129 * kD + row] = l;
     }
     if (got)
@@ -1036,6 +1051,7 @@ __global__ void __launch_bounds__(kTcwThreads, 1)
       sm_store(mine, __float_as_int(l));
       group_sync(pair_bar, 64);
       l += __int_as_float(sm_load(theirs));
+      if (!SPLIT && l == 0.f && live && row_sees<ROWS>(ta, my, ql, sm_load(met_bad) != 0)) l = CUDART_NAN_F;
       tcw_result<SPLIT>(ta, items[turn], warp, lane, to, ql, live, !gave_up && nb > 0, m, l);
       // (the next item's products write O only once its first P is there, so after these loads)
     }
@@ -1099,6 +1115,11 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
       if (k < count) add(k, early[k]);
 #pragma unroll 8
     for (int k = kEarly; k < count; ++k) add(k, record(k));
+  }
+  if (L == 0.f) {
+    TcwItem it;
+    const int idx = (b * ta.items * a.Hkv + h) * ta.tiles + pair;
+    if (tcw_item<true, ROWS>(ta, idx, it, false) && row_sees<ROWS>(ta, it, q, true)) L = CUDART_NAN_F;
   }
   const float f = L == 0.f ? 0.f : 1.f / L;  // (a sum that is not a number reaches the row: its terms above were left out)
   reinterpret_cast<uint2*>(a.out + ((size_t)(row0 + pair * 2 * ta.qpt + q) * a.Hq + h * g + head) * kD)[lane] =
