@@ -31,6 +31,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include <math_constants.h>
+
 namespace oscar {
 namespace {
 
@@ -814,7 +816,16 @@ __device__ __forceinline__ void window_body(const WindowArgs& wa) {
   __syncthreads();
   // normalise, turn back, round once
   for (int hh = warp; hh < g; hh += kW) {
-    const float f = sm_l[hh] > 0.f ? 1.f / sm_l[hh] : 0.f;
+    float sum = sm_l[hh];
+    if (sum == 0.f) {  // it sees nothing (zeros), or its logits are all -infinity (NaN)
+      bool any = false;
+      for (int u = lane; u - lane < units && !any; u += 32) {
+        const int j = u < units ? 16 * s.tile(u * KU) : s.len, end = min(j + 16 * KU, s.len);
+        any = __any_sync(0xffffffffu, j < s.len && (j < s.sinks || s.low < end) && page_of(a.pages, b, j / kPage, a.err, false) >= 0);
+      }
+      if (any) sum = CUDART_NAN_F;
+    }
+    const float f = sum != 0.f ? 1.f / sum : 0.f;
     const float4 y = reinterpret_cast<const float4*>(sm_q + hh * kD)[lane];
     float v[4] = {y.x * f, y.y * f, y.z * f, y.w * f};
     if constexpr (INT4) {

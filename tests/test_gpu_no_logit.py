@@ -9,7 +9,7 @@ from oracle import paged
 from paged_harness import attention_error, f64
 from row_errors import row_errors
 from test_gpu_prompt import Prompts, whole
-from test_gpu_window import Case
+from test_gpu_window import Case, steps
 
 pytestmark = pytest.mark.gpu
 
@@ -91,4 +91,39 @@ def test_chunks_that_see_bad_pages_alone(count, ctx):
     assert abi.oscar_check_device_error(c.ctx) == abi.OSCAR_DEVERR_PAGE
     assert not c.out[:count].any()
     assert torch.isnan(c.out[count:, 3]).all() and not torch.isnan(c.out[count:, :3]).any()
+    c.close()
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("Hq, Hkv", [(8, 2), (3, 1), (8, 1)])
+@pytest.mark.parametrize("spans, window, sinks, rows", [
+    (steps(1, 2, 70, 900), -1, 0, [0, 1, 3]), (steps(3000, 40), 100, 3, [0, 1]), (steps(20011), -1, 0, [0]),
+    ([(0, 1, 0), (40, 1, 41), (100, 1, 50)], 10, 0, [0, 1, 2])])
+def test_tokens_over_pages(Hq, Hkv, spans, window, sinks, rows, value):
+    over_pages(Hq, Hkv, spans, window, sinks, rows, value)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("Hq, Hkv", [(8, 2), (8, 1)])
+def test_tokens_over_4_bits(Hq, Hkv, value):
+    c = Case(Hq, Hkv, steps(1, 2, 300), -1, 0, True, seed=98)
+    c.q[:, 2, 3] = value
+    c.call()
+    assert abi.oscar_check_device_error(c.ctx) == 0
+    assert torch.isnan(c.out[:, 2]).all()
+    rest = [h for h in range(Hq) if h != 2]
+    assert not torch.isnan(c.out[:, rest]).any()
+    c.close()
+
+
+@pytest.mark.parametrize("ctx", [30, 5000])  # one block's, and cut into several
+def test_tokens_that_see_bad_pages_alone(ctx):
+    c = Case(4, 1, steps(ctx, 30), -1, 0, False, seed=99)
+    c.pt[0].fill_(1 << 30)
+    c.q[:, 3, 3] = float("-inf")
+    c.k_pages[..., 3] = c.k_pages[..., 3].abs() + 1
+    c.call()
+    assert abi.oscar_check_device_error(c.ctx) == abi.OSCAR_DEVERR_PAGE
+    assert not c.out[0].any()
+    assert torch.isnan(c.out[1, 3]).all() and not torch.isnan(c.out[1, :3]).any()
     c.close()
