@@ -255,6 +255,13 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _int32(x, name):
+    """A plain integer of a call that 32 bits hold (ctypes would wrap it without a word)."""
+    if not -2147483648 <= x <= 2147483647:
+        raise ValueError("%s must be a 32-bit integer" % name)
+    return x
+
+
 def oscar_create(config):
     h = ctypes.c_void_p()
     _check(load().oscar_create(ctypes.byref(config), ctypes.byref(h)), "oscar_create")
@@ -273,51 +280,54 @@ def oscar_load_rotation(ctx, layer, U_K, U_V, tau_k, tau_v, flags=OSCAR_ROT_ALL)
     uv = np.ascontiguousarray(U_V, dtype=np.float32)
     if uk.shape != (HEAD_DIM, HEAD_DIM) or uv.shape != (HEAD_DIM, HEAD_DIM):
         raise ValueError("U_K and U_V must be [128, 128]")
-    _check(load().oscar_load_rotation(ctx, layer, uk.ctypes.data, uv.ctypes.data, float(tau_k), float(tau_v),
-                                      flags), "oscar_load_rotation")
+    _check(load().oscar_load_rotation(ctx, _int32(layer, "layer"), uk.ctypes.data, uv.ctypes.data, float(tau_k),
+                                      float(tau_v), flags), "oscar_load_rotation")
 
 
 def oscar_kv_append(ctx, layer, view, args, stream=None):
-    _check(load().oscar_kv_append(ctx, layer, ctypes.byref(view), ctypes.byref(args), _stream(stream)),
+    _check(load().oscar_kv_append(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(args), _stream(stream)),
            "oscar_kv_append")
 
 
 def oscar_decode_workspace_bytes(ctx, max_batch, max_ctx_len):
-    return int(load().oscar_decode_workspace_bytes(ctx, max_batch, max_ctx_len))
+    return int(load().oscar_decode_workspace_bytes(ctx, _int32(max_batch, "max_batch"), _int32(max_ctx_len, "max_ctx_len")))
 
 
 def oscar_decode_attention(ctx, layer, view, args, workspace, workspace_bytes, stream=None):
-    _check(load().oscar_decode_attention(ctx, layer, ctypes.byref(view), ctypes.byref(args), _ptr(workspace),
-                                         workspace_bytes, _stream(stream)), "oscar_decode_attention")
+    _check(load().oscar_decode_attention(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(args),
+                                         _ptr(workspace), workspace_bytes, _stream(stream)), "oscar_decode_attention")
 
 
 def oscar_extend_attention(ctx, layer, view, args, limit, workspace, workspace_bytes, stream=None):
     """Decode-style attention of batch rows (a chunk's queries) with per-row causal limits (device int32)."""
-    _check(load().oscar_extend_attention(ctx, layer, ctypes.byref(view), ctypes.byref(args), _ptr(limit),
+    _check(load().oscar_extend_attention(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(args), _ptr(limit),
                                          _ptr(workspace), workspace_bytes, _stream(stream)), "oscar_extend_attention")
 
 
 def oscar_extend_workspace_bytes(ctx, batch, chunk, max_ctx_len):
-    return int(load().oscar_extend_workspace_bytes(ctx, batch, chunk, max_ctx_len))
+    return int(load().oscar_extend_workspace_bytes(ctx, _int32(batch, "batch"), _int32(chunk, "chunk"),
+                                                   _int32(max_ctx_len, "max_ctx_len")))
 
 
 def oscar_extend_chunk(ctx, layer, view, q, out, ctx_len, pos0, chunk, max_ctx_len, workspace, workspace_bytes,
                        sm_scale=0.0, stream=None):
     """q bf16 [batch, chunk, Hq, 128], out fp32 (same), ctx_len and pos0 int32 [batch] (all device tensors)."""
-    _check(load().oscar_extend_chunk(ctx, layer, ctypes.byref(view), _ptr(q), _ptr(out), _ptr(ctx_len), _ptr(pos0),
-                                     chunk, max_ctx_len, float(sm_scale), _ptr(workspace), workspace_bytes,
-                                     _stream(stream)), "oscar_extend_chunk")
+    _check(load().oscar_extend_chunk(ctx, _int32(layer, "layer"), ctypes.byref(view), _ptr(q), _ptr(out), _ptr(ctx_len),
+                                     _ptr(pos0), _int32(chunk, "chunk"), _int32(max_ctx_len, "max_ctx_len"),
+                                     float(sm_scale), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "oscar_extend_chunk")
 
 
 def oscar_decode_step(ctx, layer, view, append, decode, workspace, workspace_bytes, stream=None):
     """Append one token per request, then decode, in one launch."""
-    _check(load().oscar_decode_step(ctx, layer, ctypes.byref(view), ctypes.byref(append), ctypes.byref(decode),
-                                    _ptr(workspace), workspace_bytes, _stream(stream)), "oscar_decode_step")
+    _check(load().oscar_decode_step(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(append),
+                                    ctypes.byref(decode), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "oscar_decode_step")
 
 
 def oscar_decode_attention_noalloc(ctx, layer, view, args, stream=None):
     """Decode with the library's built-in scratch array instead of a caller workspace."""
-    _check(load().oscar_decode_attention_noalloc(ctx, layer, ctypes.byref(view), ctypes.byref(args),
+    _check(load().oscar_decode_attention_noalloc(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(args),
                                                  _stream(stream)), "oscar_decode_attention_noalloc")
 
 
@@ -327,13 +337,15 @@ def oscar_decode_attention_bf16(ctx, view, args, workspace, workspace_bytes, str
 
 
 def oscar_calib_workspace_bytes(n_queries, n_keys, n_kv_heads, n_clip_rows):
-    return int(load().oscar_calib_workspace_bytes(n_queries, n_keys, n_kv_heads, n_clip_rows))
+    return int(load().oscar_calib_workspace_bytes(_int32(n_queries, "n_queries"), _int32(n_keys, "n_keys"),
+                                                  _int32(n_kv_heads, "n_kv_heads"), _int32(n_clip_rows, "n_clip_rows")))
 
 
 def oscar_calib_covariances(ctx, q, n_q, k, v, n_k, n_kv_heads, sm_scale, c_q, c_s, workspace, workspace_bytes,
                             stream=None):
     """q [n_q, 128], k and v [heads, n_k, 128] device float32; c_q, c_s device float64 [128, 128]."""
-    _check(load().oscar_calib_covariances(ctx, _ptr(q), n_q, _ptr(k), _ptr(v), n_k, n_kv_heads, float(sm_scale),
+    _check(load().oscar_calib_covariances(ctx, _ptr(q), _int32(n_q, "n_q"), _ptr(k), _ptr(v), _int32(n_k, "n_k"),
+                                          _int32(n_kv_heads, "n_kv_heads"), float(sm_scale),
                                           _ptr(c_q), _ptr(c_s), _ptr(workspace), workspace_bytes, _stream(stream)),
            "oscar_calib_covariances")
 
@@ -345,7 +357,7 @@ def oscar_calib_clip_threshold(ctx, x, n_rows, U, flags, percentile, workspace, 
     if u.shape != (HEAD_DIM, HEAD_DIM):
         raise ValueError("U must be [128, 128]")
     tau = ctypes.c_double(0.0)
-    _check(load().oscar_calib_clip_threshold(ctx, _ptr(x), n_rows, u.ctypes.data, flags, float(percentile),
+    _check(load().oscar_calib_clip_threshold(ctx, _ptr(x), _int32(n_rows, "n_rows"), u.ctypes.data, flags, float(percentile),
                                              ctypes.byref(tau), _ptr(workspace), workspace_bytes, _stream(stream)),
            "oscar_calib_clip_threshold")
     return float(tau.value)
@@ -397,29 +409,30 @@ def oscar_rope_append_int4(ctx, view, args, stream=None):
            "oscar_rope_append_int4")
 
 
-_int32 = None  # torch.int32, once a tensor has been seen (naming a type takes as long as a launch)
+_torch_int32 = None  # torch.int32, once a tensor has been seen (naming a type takes as long as a launch)
 
 
 def _is_int32(dtype):
-    global _int32
+    global _torch_int32
     if str(dtype) == "torch.int32":
-        _int32 = dtype
-    return dtype is _int32
+        _torch_int32 = dtype
+    return dtype is _torch_int32
 
 
 def oscar_int4_to_bf16(ctx, from_view, to_view, pos, count, max_count, stream=None):
     """Read positions [pos, pos + count) of every request (device int32) back from the 4-bit cache into BF16 pages."""
     if pos is not None and pos.__class__ is not int:  # a tensor, not an address
-        if (pos.dtype is not _int32 and not _is_int32(pos.dtype)) or pos.numel() < from_view.batch or not pos.is_contiguous():
+        if (pos.dtype is not _torch_int32 and not _is_int32(pos.dtype)) or pos.numel() < from_view.batch or (
+                not pos.is_contiguous()):
             raise ValueError("pos must be a contiguous int32 tensor with an entry for each request")
         pos = pos.data_ptr()
     if count is not None and count.__class__ is not int:
-        if (count.dtype is not _int32 and not _is_int32(count.dtype)) or count.numel() < from_view.batch or (
+        if (count.dtype is not _torch_int32 and not _is_int32(count.dtype)) or count.numel() < from_view.batch or (
                 not count.is_contiguous()):
             raise ValueError("count must be a contiguous int32 tensor with an entry for each request")
         count = count.data_ptr()
-    _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), pos, count, max_count,
-                                     _stream(stream)), "oscar_int4_to_bf16")
+    _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), pos, count,
+                                     _int32(max_count, "max_count"), _stream(stream)), "oscar_int4_to_bf16")
 
 
 def oscar_window_workspace_bytes(ctx):
@@ -448,7 +461,7 @@ def _per_request(x, batch, name):
     """The address of a device int32 tensor with an entry for each request (or an address as it is)."""
     if x is None or x.__class__ is int:
         return x
-    if (x.dtype is not _int32 and not _is_int32(x.dtype)) or x.numel() < batch or not x.is_contiguous():
+    if (x.dtype is not _torch_int32 and not _is_int32(x.dtype)) or x.numel() < batch or not x.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor with an entry for each request" % name)
     return x.data_ptr()
 
@@ -457,9 +470,10 @@ def oscar_int2_to_bf16(ctx, layer, from_view, to_view, ctx_len, pos, count, max_
     """Read positions [pos, pos + count) of every request (device int32) back from the mixed cache of ctx_len positions
     into BF16 pages."""
     batch = from_view.batch
-    _check(load().oscar_int2_to_bf16(ctx, layer, ctypes.byref(from_view), ctypes.byref(to_view),
+    _check(load().oscar_int2_to_bf16(ctx, _int32(layer, "layer"), ctypes.byref(from_view), ctypes.byref(to_view),
                                      _per_request(ctx_len, batch, "ctx_len"), _per_request(pos, batch, "pos"),
-                                     _per_request(count, batch, "count"), max_count, _stream(stream)), "oscar_int2_to_bf16")
+                                     _per_request(count, batch, "count"), _int32(max_count, "max_count"), _stream(stream)),
+           "oscar_int2_to_bf16")
 
 
 def oscar_selftest_bounded_wait(ctx, polls, stream=None):

@@ -114,7 +114,7 @@ def append_args(k, v, pos, cu_seqlens=None, max_tokens_per_req=None, fresh_ring=
     a = abi.oscar_append_args(
         k=k.data_ptr(), v=v.data_ptr(), pos=pos.data_ptr(),
         cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr(), n_tokens=n,
-        max_tokens_per_req=n if max_tokens_per_req is None else int(max_tokens_per_req),
+        max_tokens_per_req=n if max_tokens_per_req is None else _int32(max_tokens_per_req, "max_tokens_per_req"),
         flags=abi.OSCAR_APPEND_FRESH_RING if fresh_ring else 0)
     a._tensors = (k, v, pos, cu_seqlens)
     return a
@@ -123,7 +123,7 @@ def append_args(k, v, pos, cu_seqlens=None, max_tokens_per_req=None, fresh_ring=
 def decode_args(q, out, ctx_len, max_ctx_len, sm_scale=0.0):
     """oscar_decode_args; the struct keeps q, out and ctx_len alive (it holds their addresses)."""
     a = abi.oscar_decode_args(q=q.data_ptr(), out=out.data_ptr(), ctx_len=ctx_len.data_ptr(),
-                              max_ctx_len=int(max_ctx_len), sm_scale=float(sm_scale))
+                              max_ctx_len=_int32(max_ctx_len, "max_ctx_len"), sm_scale=float(sm_scale))
     a._tensors = (q, out, ctx_len)
     return a
 
@@ -208,10 +208,7 @@ def _token_stride(x, name):
 
 def _int32(x, name):
     """x as an int that the ABI's 32 bits hold (beyond them it would wrap)."""
-    x = int(x)
-    if not -2 ** 31 <= x < 2 ** 31:
-        raise ValueError("%s must be a 32-bit integer" % name)
-    return x
+    return abi._int32(int(x), name)
 
 
 _SCALINGS = {"linear": abi.OSCAR_ROPE_LINEAR, "ntk": abi.OSCAR_ROPE_NTK, "turns": abi.OSCAR_ROPE_TURNS,
@@ -304,7 +301,7 @@ def rope_append_args(k, v, pos, q=None, q_out=None, rope=None, interleaved=False
         rope_positions=0 if rope is None else rope.shape[0], rotary_dim=0 if rope is None else rope.shape[1],
         interleaved=1 if interleaved else 0, pos=pos.data_ptr(),
         cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr(), n_tokens=n,
-        max_tokens_per_req=n if max_tokens_per_req is None else int(max_tokens_per_req))
+        max_tokens_per_req=n if max_tokens_per_req is None else _int32(max_tokens_per_req, "max_tokens_per_req"))
     a._tensors = (q, q_out, k, v, rope, pos, cu_seqlens)
     return a
 
@@ -323,8 +320,10 @@ def window_args(q, out, pos, ctx_len, max_ctx_len, window=-1, sinks=0, cu_seqlen
         q=q.data_ptr(), out=out.data_ptr(), pos=pos.data_ptr(),
         cu_seqlens=None if cu_seqlens is None else cu_seqlens.data_ptr(), ctx_len=ctx_len.data_ptr(),
         q_stride=_token_stride(q, "q"), n_tokens=n,
-        max_tokens_per_req=(1 if cu_seqlens is None else n) if max_tokens_per_req is None else int(max_tokens_per_req),
-        max_ctx_len=int(max_ctx_len), window=int(window), sinks=int(sinks), sm_scale=float(sm_scale))
+        max_tokens_per_req=(1 if cu_seqlens is None else n) if max_tokens_per_req is None
+        else _int32(max_tokens_per_req, "max_tokens_per_req"),
+        max_ctx_len=_int32(max_ctx_len, "max_ctx_len"), window=_int32(window, "window"), sinks=_int32(sinks, "sinks"),
+        sm_scale=float(sm_scale))
     a._tensors = (q, out, pos, cu_seqlens, ctx_len)
     return a
 
