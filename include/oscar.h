@@ -235,7 +235,9 @@ void oscar_destroy(oscar_ctx* ctx);
  * tau / 1.5 must fit fp16 (tau <= 98256).  The library forms the composite
  * R = U H P of the enabled factors (flags) in double precision and keeps R_K,
  * R_V and R_V^T in fp32 on the device; every kernel applies the rotation as
- * one dense product with R.  Synchronous (copies before return).
+ * one dense product with R.  Synchronous: the copies are complete on return,
+ * for calls on any stream.  A layer that is loaded again must not be in use by
+ * calls still running.
  */
 oscar_status oscar_load_rotation(oscar_ctx* ctx, int32_t layer, const float* U_K, const float* U_V,
                                  float tau_k, float tau_v, uint32_t flags);

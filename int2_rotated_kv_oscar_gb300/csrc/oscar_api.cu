@@ -146,7 +146,8 @@ oscar_status oscar_create(const oscar_config* cfg, oscar_ctx** out) {
   if (ctx == nullptr) return OSCAR_ERR_CUDA;
   ctx->cfg = *cfg;
   if (cudaDeviceGetAttribute(&ctx->num_sms, cudaDevAttrMultiProcessorCount, cfg->device) != cudaSuccess ||
-      cudaMalloc(&ctx->d_err, sizeof(unsigned)) != cudaSuccess || cudaMemset(ctx->d_err, 0, sizeof(unsigned)) != cudaSuccess) {
+      cudaMalloc(&ctx->d_err, sizeof(unsigned)) != cudaSuccess || cudaMemset(ctx->d_err, 0, sizeof(unsigned)) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess) {  // (as at the end of oscar_load_rotation)
     if (ctx->d_err) cudaFree(ctx->d_err);
     delete ctx;
     return OSCAR_ERR_CUDA;
@@ -235,6 +236,9 @@ oscar_status oscar_load_rotation(oscar_ctx* ctx, int32_t layer, const float* U_K
           cudaSuccess ||
       cudaMemcpy(ctx->d_rot[layer] + 6 * n, image.data(), sizeof(uint16_t) * 4 * n, cudaMemcpyHostToDevice) != cudaSuccess)
     return OSCAR_ERR_CUDA;
+  // A copy from pageable memory may return once its source is staged, and a stream that does not wait for the default
+  // one would read what is still under way (kernels read these constants ahead of their wait for the work before them).
+  if (cudaStreamSynchronize(nullptr) != cudaSuccess) return OSCAR_ERR_CUDA;
   ctx->tau_k[layer] = tau_k;
   ctx->tau_v[layer] = tau_v;
   ctx->rot_flags[layer] = flags;

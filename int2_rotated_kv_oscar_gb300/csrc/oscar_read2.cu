@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kRdThreads, 1)
   bool ok = true;
 
   if (warp == kRdCopy) {
-    if (lane == 0) {  // (R does not depend on the work ahead in the stream: it was uploaded synchronously)
+    if (lane == 0) {  // (R does not depend on the work ahead in the stream: oscar_load_rotation returns with its copies complete)
       mbar_arrive_expect_tx(rfull, 65536);
       bulk_copy_g2s(sm + kRdR, a.r_image + (is_v ? 32768 : 0), 65536, rfull);
     }
