@@ -573,8 +573,8 @@ cudaError_t launch_int2_to_bf16(const Read2Launch& a, cudaStream_t stream) {
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
-  // at most: a request's rows touch (max_count + 126) / 64 pages
-  const long long pages = ((long long)a.max_count + 126) / kPage, pairs = (pages + 1) / 2;
+  // at most: a request's rows touch (max_count + 126) / 64 pages, and no more than its table has (a loose bound is no error)
+  const long long pages = std::min(((long long)a.max_count + 126) / kPage, (long long)a.to.max_pages), pairs = (pages + 1) / 2;
   const long long tiles = pairs * Hkv * a.from.batch;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   Read2Launch la = a;
