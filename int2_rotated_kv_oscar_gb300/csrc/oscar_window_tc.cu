@@ -1203,7 +1203,9 @@ static cudaError_t launch_tc(const WindowLaunch& a, const KeyRows* rows, int bat
   ta.qpt = 128 / ta.g;
   ta.tiles = (a.tok.max_tokens + 2 * ta.qpt - 1) / (2 * ta.qpt);
   ta.by_tiles = Divisor(ta.tiles);
-  const long long total = (long long)ta.tiles * batch * a.Hkv * ta.items;
+  long long total = (long long)ta.tiles * batch * a.Hkv * ta.items;
+  // (whole items over packed rows are counted on the device, n_tokens Hkv at most: a loose bound is no error)
+  if (rows != nullptr && !split) total = std::min<long long>(total, INT32_MAX - 65536);
   if (total > INT32_MAX - 65536) return cudaErrorInvalidValue;
   ta.total = (int)total;
   {  // the queries as [n_tokens][Hq][128], boxes of 64 channels x one KV head's g heads x a tile's queries
