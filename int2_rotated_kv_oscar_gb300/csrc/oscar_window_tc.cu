@@ -42,9 +42,9 @@
 // and first blocks 6200, with the result on its way to memory (2700) in between.
 // For seconds on end, the board's power limit (1.7 to 1.8 GHz instead of 2.05).
 // Three prompts of up to 12K tokens over pages (window 4096, 32 query heads):
-// 1.00 ms, 1.57 PFLOP/s; 256 tokens at 100,000: 261 us.  In packed rows: one
-// prompt of 24,001 tokens 2.5 to 2.8 ms, 1.68 to 1.85 PFLOP/s, 48 prompts of 1 to
-// 2048 tokens 436 us (477 for seconds).
+// 0.98 ms, 1.58 PFLOP/s; 256 tokens at 100,000: 257 us.  In packed rows: one
+// prompt of 24,001 tokens 2.5 to 2.8 ms, 1.66 to 1.92 PFLOP/s, 48 prompts of 1 to
+// 2048 tokens 437 us (490 to 500 for seconds).
 // Tried when the first took 1.19: all sixteen warps on one tile at a time (a
 // quarter of a row a thread), 1.32 ms, since the loads and votes then lie bare;
 // the next logits' loads under the exponentials, 1.22 ms.  When the 48 prompts took
