@@ -256,7 +256,8 @@ def _stream(stream):
 
 
 def _int32(x, name):
-    """A plain integer of a call that 32 bits hold (ctypes would wrap it without a word)."""
+    """A plain integer of a call that 32 bits hold (ctypes would wrap it without a word).  Calls of a few microseconds
+    compare for themselves and come here when it does not fit."""
     if not -2147483648 <= x <= 2147483647:
         raise ValueError("%s must be a 32-bit integer" % name)
     return x
@@ -285,7 +286,9 @@ def oscar_load_rotation(ctx, layer, U_K, U_V, tau_k, tau_v, flags=OSCAR_ROT_ALL)
 
 
 def oscar_kv_append(ctx, layer, view, args, stream=None):
-    _check(load().oscar_kv_append(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(args), _stream(stream)),
+    if not -2147483648 <= layer <= 2147483647:
+        _int32(layer, "layer")
+    _check(load().oscar_kv_append(ctx, layer, ctypes.byref(view), ctypes.byref(args), _stream(stream)),
            "oscar_kv_append")
 
 
@@ -294,7 +297,9 @@ def oscar_decode_workspace_bytes(ctx, max_batch, max_ctx_len):
 
 
 def oscar_decode_attention(ctx, layer, view, args, workspace, workspace_bytes, stream=None):
-    _check(load().oscar_decode_attention(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(args),
+    if not -2147483648 <= layer <= 2147483647:
+        _int32(layer, "layer")
+    _check(load().oscar_decode_attention(ctx, layer, ctypes.byref(view), ctypes.byref(args),
                                          _ptr(workspace), workspace_bytes, _stream(stream)), "oscar_decode_attention")
 
 
@@ -320,14 +325,18 @@ def oscar_extend_chunk(ctx, layer, view, q, out, ctx_len, pos0, chunk, max_ctx_l
 
 def oscar_decode_step(ctx, layer, view, append, decode, workspace, workspace_bytes, stream=None):
     """Append one token per request, then decode, in one launch."""
-    _check(load().oscar_decode_step(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(append),
+    if not -2147483648 <= layer <= 2147483647:
+        _int32(layer, "layer")
+    _check(load().oscar_decode_step(ctx, layer, ctypes.byref(view), ctypes.byref(append),
                                     ctypes.byref(decode), _ptr(workspace), workspace_bytes, _stream(stream)),
            "oscar_decode_step")
 
 
 def oscar_decode_attention_noalloc(ctx, layer, view, args, stream=None):
     """Decode with the library's built-in scratch array instead of a caller workspace."""
-    _check(load().oscar_decode_attention_noalloc(ctx, _int32(layer, "layer"), ctypes.byref(view), ctypes.byref(args),
+    if not -2147483648 <= layer <= 2147483647:
+        _int32(layer, "layer")
+    _check(load().oscar_decode_attention_noalloc(ctx, layer, ctypes.byref(view), ctypes.byref(args),
                                                  _stream(stream)), "oscar_decode_attention_noalloc")
 
 
@@ -431,8 +440,10 @@ def oscar_int4_to_bf16(ctx, from_view, to_view, pos, count, max_count, stream=No
                 not count.is_contiguous()):
             raise ValueError("count must be a contiguous int32 tensor with an entry for each request")
         count = count.data_ptr()
-    _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), pos, count,
-                                     _int32(max_count, "max_count"), _stream(stream)), "oscar_int4_to_bf16")
+    if not -2147483648 <= max_count <= 2147483647:
+        _int32(max_count, "max_count")
+    _check(load().oscar_int4_to_bf16(ctx, ctypes.byref(from_view), ctypes.byref(to_view), pos, count, max_count,
+                                     _stream(stream)), "oscar_int4_to_bf16")
 
 
 def oscar_window_workspace_bytes(ctx):
@@ -470,10 +481,11 @@ def oscar_int2_to_bf16(ctx, layer, from_view, to_view, ctx_len, pos, count, max_
     """Read positions [pos, pos + count) of every request (device int32) back from the mixed cache of ctx_len positions
     into BF16 pages."""
     batch = from_view.batch
-    _check(load().oscar_int2_to_bf16(ctx, _int32(layer, "layer"), ctypes.byref(from_view), ctypes.byref(to_view),
+    if not (-2147483648 <= layer <= 2147483647 and -2147483648 <= max_count <= 2147483647):
+        _int32(layer, "layer"), _int32(max_count, "max_count")
+    _check(load().oscar_int2_to_bf16(ctx, layer, ctypes.byref(from_view), ctypes.byref(to_view),
                                      _per_request(ctx_len, batch, "ctx_len"), _per_request(pos, batch, "pos"),
-                                     _per_request(count, batch, "count"), _int32(max_count, "max_count"), _stream(stream)),
-           "oscar_int2_to_bf16")
+                                     _per_request(count, batch, "count"), max_count, _stream(stream)), "oscar_int2_to_bf16")
 
 
 def oscar_selftest_bounded_wait(ctx, polls, stream=None):
